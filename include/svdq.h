@@ -326,6 +326,122 @@ SVDQ_API svdq_status svdq_w4a16_export(svdq_w4a16_t layer, void* codes, void* sc
 /* Frees the layer (synchronizes the device first). */
 SVDQ_API svdq_status svdq_w4a16_destroy(svdq_w4a16_t layer);
 
+/* ------------------------------------------------------------------------
+ * The rest of a transformer block around the quantized layers: attention
+ * between the QKV and output projections, the layers that stay in 16 bits,
+ * and the norms with the block's gate and residual. These calls keep no state
+ * and own nothing: every buffer is the caller's, and calls on different
+ * streams are independent (each with its own workspace). All device pointers
+ * and the stream belong to the current device. Sequences are packed without
+ * padding: sequence b of a batch owns rows [offsets[b], offsets[b + 1]), with
+ * offsets on the device (they are never read on the host; the calls can be
+ * captured into a graph). offsets must start at 0 or above and not decrease;
+ * values outside [0, rows] are clamped, so that no access leaves the tensors. */
+typedef enum {
+  SVDQ_BF16 = 0,
+  SVDQ_F16 = 1,
+  SVDQ_F32 = 2
+} svdq_dtype;
+
+/* Attention of packed sequences with grouped heads:
+ *     o_i = sum_j softmax_j(scale <q_i, k_j>) v_j
+ * over the keys j of the query's own sequence; with `causal`, query i of Lq
+ * sees keys j <= i + Lk - Lq (the last query sees every key, so a sequence's
+ * queries may be a whole prompt, a piece of one, or a single new token against
+ * all the keys so far). A query that sees no key gives 0. Keys a query does not
+ * see never reach its result, whatever they hold (infinities and NaN
+ * included). Query head h reads key head h / (q_heads / kv_heads).
+ * Scores, softmax statistics and sums are float; the probabilities are rounded
+ * to `dtype` for the product with V. */
+typedef struct {
+  int dtype;               /* SVDQ_BF16 or SVDQ_F16: q, k, v and out */
+  int batch;               /* sequences, >= 1 */
+  int q_rows, k_rows;      /* rows of q / out and of k, v, all sequences together, >= 0 */
+  int q_heads, kv_heads;   /* q_heads a multiple of kv_heads, at most 128 times it */
+  int head_dim;            /* a multiple of 8, 8..128 */
+  int causal;              /* 0 or 1 */
+  float scale;             /* positive and finite */
+  /* elements from one row (token) to the next and from one head to the next;
+     multiples of 8. The values of a head are contiguous. out is contiguous
+     [q_rows, q_heads, head_dim]. */
+  long long q_row_stride, q_head_stride;
+  long long k_row_stride, k_head_stride;
+  long long v_row_stride, v_head_stride;
+} svdq_attention_config;
+
+/* Bytes of workspace svdq_attention_forward needs (it depends on the device's
+ * SM count: query it on the device of the call; 0 is possible). */
+SVDQ_API svdq_status svdq_attention_workspace_size(const svdq_attention_config* cfg, size_t* bytes);
+/*   q          device [q_rows, q_heads, head_dim] with cfg's strides
+ *   k, v       device [k_rows, kv_heads, head_dim] with cfg's strides
+ *   q_offsets, k_offsets  device int32 [batch + 1]; NULL only for batch 1 (all rows)
+ *   out        device [q_rows, q_heads, head_dim]; overlaps no input. Rows that
+ *              belong to no sequence are left as they are.
+ *   workspace  at least svdq_attention_workspace_size bytes, 256-byte aligned,
+ *              no initialisation needed (may be NULL when the size is 0).
+ * q, k, v and out 16-byte aligned. One kernel on `stream`, or two where the
+ * keys of few queries are split over the SMs and joined. */
+SVDQ_API svdq_status svdq_attention_forward(const svdq_attention_config* cfg, const void* q, const void* k,
+                                            const void* v, const int* q_offsets, const int* k_offsets, void* out,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+typedef enum {
+  SVDQ_ACT_NONE = 0,
+  SVDQ_ACT_RELU = 1,
+  SVDQ_ACT_SILU = 2,       /* t / (1 + exp(-t)) */
+  SVDQ_ACT_GELU = 3,       /* t (1 + erf(t / sqrt 2)) / 2 */
+  SVDQ_ACT_GELU_TANH = 4   /* t (1 + tanh(sqrt(2 / pi) (t + 0.044715 t^3))) / 2 */
+} svdq_activation;
+
+/* A linear layer whose weight stays in 16 bits, read in place:
+ *     Y = residual + act(X W + bias)
+ * with float accumulation, and one rounding at the end.
+ *   dtype     SVDQ_BF16 or SVDQ_F16, of every tensor
+ *   X         device [M, K];  W device [K, N];  K and N multiples of 8
+ *   bias      device [N] or NULL
+ *   residual  device [M, N] or NULL
+ *   Y         device [M, N]; may be the residual itself, overlaps nothing else
+ * All 16-byte aligned. M = 0 is allowed (nothing happens). One kernel on `stream`. */
+SVDQ_API svdq_status svdq_dense_linear_forward(int dtype, const void* X, const void* W, const void* bias,
+                                               const void* residual, int activation, int M, int K, int N, void* Y,
+                                               void* stream);
+
+typedef enum {
+  SVDQ_NORM_NONE = 0,
+  SVDQ_NORM_LAYER = 1,     /* (v - mean) / sqrt(var + eps) */
+  SVDQ_NORM_RMS = 2        /* v / sqrt(mean(v^2) + eps) */
+} svdq_norm;
+
+/* The norms before and after a block, with the block's gate and residual. For
+ * a row (token) of sequence b:
+ *     x' = residual_scale x + gate[b] * (N_post(y) post_weight + post_bias)
+ *     h  = (N(x') weight + bias) * (1 + scale[b]) + shift[b]
+ * x is the residual stream, y the block's output, h the next block's input.
+ * Statistics and arithmetic are float; h comes from the unrounded x'. */
+typedef struct {
+  int dtype;               /* SVDQ_BF16 or SVDQ_F16: y, h_out and every vector */
+  int x_dtype;             /* x and x_out: dtype, or SVDQ_F32 */
+  int rows, dim;           /* dim 1..16384 */
+  int seqs;                /* rows of gate, scale and shift, >= 1 */
+  int post_norm, norm;     /* svdq_norm */
+  float residual_scale, eps;
+  const void* x;           /* device [rows, dim] */
+  const void* y;           /* device [rows, dim], or NULL: x' = x (x_out NULL, nothing of the post norm set, residual_scale 1) */
+  void* x_out;             /* device [rows, dim]; may be x */
+  void* h_out;             /* device [rows, dim]; may be y; NULL exactly when norm is SVDQ_NORM_NONE */
+  const void* gate;        /* device [seqs, dim] or NULL (1) */
+  const void *post_weight, *post_bias, *weight, *bias; /* device [dim] or NULL */
+  const void *scale, *shift; /* device [seqs, dim] or NULL */
+  const int* offsets;      /* device int32 [seqs + 1]; NULL only for seqs 1 (all rows). Rows of no sequence are left as they are. */
+} svdq_residual_norm_args;
+
+/* All tensors contiguous and 16-byte aligned. One kernel on `stream`. */
+SVDQ_API svdq_status svdq_residual_norm(const svdq_residual_norm_args* args, void* stream);
+
+/* Reads and clears the current device's status word of the calls of this
+ * section, as svdq_device_status does for a layer (synchronizes `stream`). */
+SVDQ_API svdq_status svdq_operator_status(void* stream);
+
 /* Test hook for failure detection: the library's device allocation number
  * `index` (0 = the next one) fails with SVDQ_ERR_OOM as if the device were out
  * of memory, so that tests can check that every allocating call unwinds

@@ -67,6 +67,20 @@ class _BlobHeader(ctypes.Structure):
                 ("off_bias", ctypes.c_uint64), ("total", ctypes.c_uint64)]
 
 
+class _Attention(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("batch", ctypes.c_int), ("q_rows", ctypes.c_int), ("k_rows", ctypes.c_int),
+                ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("causal", ctypes.c_int), ("scale", ctypes.c_float)] + [
+                    (f"{t}_{a}_stride", ctypes.c_longlong) for t in "qkv" for a in ("row", "head")]
+
+
+class _ResidualNorm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "x_dtype", "rows", "dim", "seqs", "post_norm", "norm")] + [
+        (n, ctypes.c_float) for n in ("residual_scale", "eps")] + [
+            (n, ctypes.c_void_p) for n in ("x", "y", "x_out", "h_out", "gate", "post_weight", "post_bias", "weight",
+                                           "bias", "scale", "shift", "offsets")]
+
+
 # Every symbol include/svdq.h declares, with its ctypes signature.
 _VP, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 SIGNATURES = {
@@ -96,6 +110,11 @@ SIGNATURES = {
     "svdq_w4a16_forward": [_VP, _VP, _I, _VP, _VP],
     "svdq_w4a16_export": [_VP, _VP, _VP, _VP],
     "svdq_w4a16_destroy": [_VP],
+    "svdq_attention_workspace_size": [ctypes.POINTER(_Attention), ctypes.POINTER(_SZ)],
+    "svdq_attention_forward": [ctypes.POINTER(_Attention), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP],
+    "svdq_dense_linear_forward": [_I, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP],
+    "svdq_residual_norm": [ctypes.POINTER(_ResidualNorm), _VP],
+    "svdq_operator_status": [_VP],
 }
 
 
@@ -450,3 +469,215 @@ class MlpBlock:
         return out
 
     __call__ = forward
+
+
+# ---------------------------------------------------------------- around the quantized layers
+_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_ACTIVATION = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+_NORM = {None: 0, "layer": 1, "rms": 2}
+
+
+def _operand(name: str, t: torch.Tensor, dtype: torch.dtype, device: torch.device, *shape) -> int:
+    """The address of a contiguous tensor of this type, place and shape."""
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _offsets(name: str, t: torch.Tensor, device: torch.device) -> int:
+    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or t.shape[0] < 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 [sequences + 1] tensor on {device}")
+    return t.data_ptr()
+
+
+class _Call:
+    """The device and stream of a call that keeps no handle: the device of its
+    tensors is made current, and what the call allocates stays valid for the
+    stream it runs on."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        self.device = t.device
+        current = torch.cuda.current_stream(t.device).cuda_stream
+        self.stream = current if stream is None else _stream(stream)
+        self._other = self.stream != current
+        self._guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+    def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self._other:
+            t.record_stream(torch.cuda.ExternalStream(self.stream, self.device))
+        return t
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self
+
+    def __exit__(self, *error):
+        if self._guard is not None:
+            self._guard.__exit__(*error)
+
+
+def _attention_config(q, k, v, batch, causal, scale) -> _Attention:
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or q.shape[2] != k.shape[2]:
+        raise ValueError(f"q must be [rows, heads, dim], k and v [rows, heads, dim] alike, got {tuple(q.shape)}, "
+                         f"{tuple(k.shape)}, {tuple(v.shape)}")
+    if q.dtype not in (torch.bfloat16, torch.float16) or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must all be bfloat16 or all float16")
+    if k.device != q.device or v.device != q.device:
+        raise ValueError("q, k and v must be on one device")
+    c = _Attention(_DTYPE[q.dtype], batch, q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2], int(bool(causal)),
+                   q.shape[2] ** -0.5 if scale is None else scale)
+    for n, t in (("q", q), ("k", k), ("v", v)):
+        row, head, one = t.stride()
+        if one != 1 and t.shape[2] > 1:
+            raise ValueError(f"the values of a head of {n} must be contiguous")
+        setattr(c, n + "_row_stride", row)
+        setattr(c, n + "_head_stride", head)
+    return c
+
+
+def attention_workspace_size(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, batch: int = 1) -> int:
+    """Bytes of workspace attention() needs for these shapes."""
+    n = ctypes.c_size_t()
+    with _Call(q, None):
+        _check(lib().svdq_attention_workspace_size(ctypes.byref(_attention_config(q, k, v, batch, False, None)),
+                                                   ctypes.byref(n)))
+    return n.value
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Optional[torch.Tensor] = None,
+              k_offsets: Optional[torch.Tensor] = None, causal: bool = False, scale: Optional[float] = None,
+              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of packed sequences (include/svdq.h, svdq_attention_forward).
+
+    q [rows, heads, dim], k and v [rows, kv heads, dim], bfloat16 or float16; views
+    are taken as they are (a QKV projection's output need not be split up), as long
+    as a head's values are contiguous and the strides multiples of 8. Sequence b
+    owns q rows q_offsets[b] to q_offsets[b + 1] and k rows k_offsets[b] to
+    k_offsets[b + 1] (int32 on the device; k_offsets defaults to q_offsets, and
+    without either all rows are one sequence). causal: the last query of a
+    sequence sees every key, the one before it all but one, and so on. scale
+    defaults to dim ** -0.5. Rows of `out` that belong to no sequence are not
+    written."""
+    with _Call(q, stream) as call:
+        if q_offsets is None:
+            if k_offsets is not None:
+                raise ValueError("k_offsets need q_offsets")
+            batch, qo, ko = 1, None, None
+        else:
+            qo = _offsets("q_offsets", q_offsets, q.device)
+            if k_offsets is None:
+                if q.shape[0] != k.shape[0]:
+                    raise ValueError("k has other rows than q: k_offsets are needed")
+                ko = qo
+            else:
+                ko = _offsets("k_offsets", k_offsets, q.device)
+                if k_offsets.shape != q_offsets.shape:
+                    raise ValueError("q_offsets and k_offsets must be of the same length")
+            batch = q_offsets.shape[0] - 1
+        cfg = _attention_config(q, k, v, batch, causal, scale)
+        need = ctypes.c_size_t()
+        _check(lib().svdq_attention_workspace_size(ctypes.byref(cfg), ctypes.byref(need)))
+        if out is None:
+            out = call.empty(q.shape, q.dtype)
+        o = _operand("out", out, q.dtype, q.device, *q.shape)
+        if workspace is None:
+            workspace = call.empty(need.value, torch.uint8)
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != q.device:
+            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+        _check(lib().svdq_attention_forward(ctypes.byref(cfg), q.data_ptr(), k.data_ptr(), v.data_ptr(), qo, ko, o,
+                                            workspace.data_ptr(), workspace.numel(), call.stream))
+    return out
+
+
+def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, activation: Optional[str] = None,
+           residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """residual + activation(X W + bias) for a layer whose weight stays in 16 bits
+    (include/svdq.h, svdq_dense_linear_forward): X [M, K], W [K, N], bias [N],
+    residual and out [M, N], all bfloat16 or all float16; activation None, "relu",
+    "silu", "gelu" or "gelu_tanh". out may be the residual."""
+    if X.dim() != 2 or W.dim() != 2 or X.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("X and W must be bfloat16 or float16 matrices")
+    if activation not in _ACTIVATION:
+        raise ValueError(f"unknown activation {activation!r}")
+    with _Call(X, stream) as call:
+        (M, K), N = X.shape, W.shape[1]
+        x = _operand("X", X, X.dtype, X.device, M, K)
+        w = _operand("W", W, X.dtype, X.device, K, N)
+        b = None if bias is None else _operand("bias", bias, X.dtype, X.device, N)
+        r = None if residual is None else _operand("residual", residual, X.dtype, X.device, M, N)
+        if out is None:
+            out = call.empty((M, N), X.dtype)
+        y = _operand("out", out, X.dtype, X.device, M, N)
+        _check(lib().svdq_dense_linear_forward(_DTYPE[X.dtype], x, w, b, r, _ACTIVATION[activation], M, K, N, y,
+                                               call.stream))
+    return out
+
+
+def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0, post_norm: Optional[str] = None,
+                  post_weight: Optional[torch.Tensor] = None, post_bias: Optional[torch.Tensor] = None,
+                  norm: Optional[str] = "rms", weight: Optional[torch.Tensor] = None,
+                  bias: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                  shift: Optional[torch.Tensor] = None, eps: float = 1e-6, dtype: Optional[torch.dtype] = None,
+                  out_x: Optional[torch.Tensor] = None, out_h: Optional[torch.Tensor] = None, stream=None):
+    """The norms after and before a block with the block's gate and residual
+    (include/svdq.h, svdq_residual_norm); returns (x', h):
+
+        x' = residual_scale x + gate * post_norm(y)
+        h  = norm(x') * (1 + scale) + shift
+
+    x [rows, dim] is the residual stream (float32, or the type of y), y the
+    block's output. Norms are "layer", "rms" or None, with weights and biases of
+    [dim]. gate, scale and shift are [sequences, dim], row b for the tokens
+    offsets[b] to offsets[b + 1] (without offsets, one row for all). Without y
+    (the first norm of a model) x' is x itself and only h is computed, in `dtype`
+    (that of x where x is not float32); with norm None h is None. out_x may be x,
+    out_h may be y. Rows that belong to no sequence are not written."""
+    if x.dim() != 2 or x.dtype not in _DTYPE:
+        raise ValueError("x must be a [rows, dim] tensor of bfloat16, float16 or float32")
+    if norm not in _NORM or post_norm not in _NORM:
+        raise ValueError(f"unknown norm {norm if norm not in _NORM else post_norm!r}")
+    rows, dim = x.shape
+    kind = y.dtype if y is not None else dtype if dtype is not None else x.dtype
+    if kind not in (torch.bfloat16, torch.float16) or x.dtype not in (kind, torch.float32):
+        raise ValueError("y and h must be bfloat16 or float16, x of the same type or float32")
+    if dtype is not None and dtype != kind:
+        raise ValueError("dtype must be that of y")
+    with _Call(x, stream) as call:
+        a = _ResidualNorm(_DTYPE[kind], _DTYPE[x.dtype], rows, dim, 1, _NORM[post_norm], _NORM[norm], residual_scale, eps)
+        a.x = _operand("x", x, x.dtype, x.device, rows, dim)
+        if offsets is not None:
+            a.offsets = _offsets("offsets", offsets, x.device)
+            a.seqs = offsets.shape[0] - 1
+        for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("weight", weight), ("bias", bias)):
+            if t is not None:
+                setattr(a, name, _operand(name, t, kind, x.device, dim))
+        for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+            if t is not None:
+                shape = (dim,) if t.dim() == 1 and a.seqs == 1 else (a.seqs, dim)
+                setattr(a, name, _operand(name, t, kind, x.device, *shape))
+        if y is not None:
+            a.y = _operand("y", y, kind, x.device, rows, dim)
+            if out_x is None:
+                out_x = call.empty((rows, dim), x.dtype)
+            a.x_out = _operand("out_x", out_x, x.dtype, x.device, rows, dim)
+        elif out_x is not None:
+            raise ValueError("without y there is no out_x")
+        if norm is not None:
+            if out_h is None:
+                out_h = call.empty((rows, dim), kind)
+            a.h_out = _operand("out_h", out_h, kind, x.device, rows, dim)
+        elif out_h is not None:
+            raise ValueError("without a norm there is no out_h")
+        _check(lib().svdq_residual_norm(ctypes.byref(a), call.stream))
+    return x if y is None else out_x, out_h
+
+
+def operator_status(stream=None) -> Status:
+    """Reads and clears the current device's status word of attention and linear."""
+    return Status(lib().svdq_operator_status(_stream(stream)))

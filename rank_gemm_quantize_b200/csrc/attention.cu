@@ -1,0 +1,160 @@
+// Host side of the attention calls: argument checks, tensor maps, the choice
+// of the kernel and of the shares the keys are cut into.
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "attention.cuh"
+
+namespace svdq {
+void set_last_error(const std::string& msg);
+cudaError_t take_status_dense(int* status, cudaStream_t st);
+}  // namespace svdq
+
+using namespace svdq;
+
+namespace {
+
+svdq_status fail(svdq_status st, const std::string& msg) {
+  set_last_error(msg);
+  return st;
+}
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+svdq_status check(const svdq_attention_config* c) {
+  if (!c) return fail(SVDQ_ERR_INVALID_ARG, "cfg is NULL");
+  if (c->dtype != SVDQ_BF16 && c->dtype != SVDQ_F16) return fail(SVDQ_ERR_INVALID_ARG, "unknown dtype");
+  if (c->batch < 1 || c->q_rows < 0 || c->k_rows < 0) return fail(SVDQ_ERR_INVALID_ARG, "bad batch, q_rows or k_rows");
+  if (c->batch > 65535) return fail(SVDQ_ERR_UNSUPPORTED, "batch exceeds 65535");
+  if (c->q_heads < 1 || c->kv_heads < 1 || c->q_heads % c->kv_heads || c->q_heads / c->kv_heads > 128)
+    return fail(SVDQ_ERR_INVALID_ARG, "q_heads must be 1 to 128 times kv_heads");
+  if (c->kv_heads > 65535) return fail(SVDQ_ERR_UNSUPPORTED, "kv_heads exceeds 65535");
+  if (c->head_dim < 8 || c->head_dim > 128 || c->head_dim % 8)
+    return fail(SVDQ_ERR_INVALID_ARG, "head_dim must be a multiple of 8, 8 to 128");
+  if (c->causal != 0 && c->causal != 1) return fail(SVDQ_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (!(c->scale > 0.f) || !std::isfinite(c->scale)) return fail(SVDQ_ERR_INVALID_ARG, "scale must be positive and finite");
+  // rows and row-head pairs are counted in int
+  if (static_cast<long long>(c->q_rows) * c->q_heads > 1ll << 30 || c->k_rows > 1 << 30)
+    return fail(SVDQ_ERR_UNSUPPORTED, "q_rows x q_heads or k_rows exceeds 2^30");
+  const long long strides[] = {c->q_row_stride, c->q_head_stride, c->k_row_stride, c->k_head_stride, c->v_row_stride, c->v_head_stride};
+  const int extent[] = {c->q_rows, c->q_heads, c->k_rows, c->kv_heads, c->k_rows, c->kv_heads};
+  for (int i = 0; i < 6; ++i)  // the stride of a single row or head is not used
+    if (extent[i] > 1 && (strides[i] < 8 || strides[i] % 8 || strides[i] >= 1ll << 38))
+      return fail(SVDQ_ERR_INVALID_ARG, "strides must be positive multiples of 8 under 2^38");
+  return SVDQ_OK;
+}
+
+struct Plan {
+  int sms, chunk, max_slots, padded;
+  size_t part, ml, total;
+};
+
+// The keys of few queries are cut into shares so that every SM has several of
+// them (two CTAs an SM, four shares a CTA).
+svdq_status plan(const svdq_attention_config* c, Plan* out) {
+  int dev = 0;
+  Plan p{};
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&p.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(SVDQ_ERR_CUDA, "no usable current device");
+  }
+  p.padded = c->head_dim <= 64 ? 64 : 128;
+  const long long shares = std::max<long long>(1, 8ll * p.sms / c->kv_heads);
+  const long long keys = (c->k_rows + shares - 1) / shares;
+  p.chunk = static_cast<int>(std::max<long long>(1, (keys + kStepKeys - 1) / kStepKeys) * kStepKeys);
+  // a sequence of more than `chunk` keys has fewer than 2 keys / chunk shares
+  const long long rows = static_cast<long long>(c->q_rows) * (c->q_heads / c->kv_heads);
+  const int tiles = static_cast<int>(std::min<long long>(kSplitTiles, (rows + kStepRows - 1) / kStepRows));
+  p.max_slots = c->k_rows > p.chunk ? static_cast<int>(2ll * c->k_rows / p.chunk) * tiles : 0;
+  const size_t slot_rows = static_cast<size_t>(p.max_slots) * c->kv_heads * kStepRows;
+  p.part = 0;
+  p.ml = slot_rows * p.padded * 4;
+  p.total = p.ml + slot_rows * 8;
+  *out = p;
+  return SVDQ_OK;
+}
+
+bool make_kv_map(CUtensorMap* m, const svdq_attention_config* c, const void* base, long long row, long long head, int keys) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim), static_cast<uint64_t>(c->kv_heads), static_cast<uint64_t>(c->k_rows)};
+  // a single head or row has no stride of its own: any legal one
+  const uint64_t strides[2] = {static_cast<uint64_t>(c->kv_heads > 1 ? head : c->head_dim) * 2,
+                               static_cast<uint64_t>(c->k_rows > 1 ? row : c->head_dim) * 2};
+  const uint32_t box[3] = {64, 1, static_cast<uint32_t>(keys)};
+  return make_map_3d(m, c->dtype == SVDQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+extern "C" {
+
+svdq_status svdq_attention_workspace_size(const svdq_attention_config* cfg, size_t* bytes) {
+  if (svdq_status e = check(cfg)) return e;
+  if (!bytes) return fail(SVDQ_ERR_INVALID_ARG, "bytes is NULL");
+  Plan p;
+  if (svdq_status e = plan(cfg, &p)) return e;
+  *bytes = p.total;
+  return SVDQ_OK;
+}
+
+svdq_status svdq_attention_forward(const svdq_attention_config* cfg, const void* q, const void* k, const void* v,
+                                   const int* q_offsets, const int* k_offsets, void* out, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  if (svdq_status e = check(cfg)) return e;
+  if (cfg->q_rows == 0) return SVDQ_OK;
+  if (!q || !out || (cfg->k_rows > 0 && (!k || !v))) return fail(SVDQ_ERR_INVALID_ARG, "q, k, v or out is NULL");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
+    return fail(SVDQ_ERR_INVALID_ARG, "q, k, v and out must be 16-byte aligned");
+  if ((!q_offsets || !k_offsets) && cfg->batch != 1) return fail(SVDQ_ERR_INVALID_ARG, "several sequences need offsets");
+  if (!aligned(q_offsets, 4) || !aligned(k_offsets, 4)) return fail(SVDQ_ERR_INVALID_ARG, "offsets must be 4-byte aligned");
+  Plan pl;
+  if (svdq_status e = plan(cfg, &pl)) return e;
+  if (pl.total && (!workspace || !aligned(workspace, 256) || workspace_bytes < pl.total))
+    return fail(SVDQ_ERR_INVALID_ARG, "workspace missing, misaligned or too small");
+  AttnParams p{};
+  p.q = q;
+  p.v = v;
+  p.out = out;
+  p.q_offsets = q_offsets;
+  p.k_offsets = k_offsets;
+  p.batch = cfg->batch;
+  p.q_rows = cfg->q_rows;
+  p.k_rows = cfg->k_rows;
+  p.q_heads = cfg->q_heads;
+  p.kv_heads = cfg->kv_heads;
+  p.group = cfg->q_heads / cfg->kv_heads;
+  p.dim = cfg->head_dim;
+  p.causal = cfg->causal;
+  p.scale_log2 = cfg->scale * 1.4426950408889634f;
+  p.q_row = cfg->q_row_stride;
+  p.q_head = cfg->q_head_stride;
+  p.v_row = cfg->v_row_stride;
+  p.v_head = cfg->v_head_stride;
+  p.chunk = pl.chunk;
+  p.max_slots = pl.max_slots;
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.part);
+  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.ml);
+  AttnMaps maps{};
+  if (cfg->k_rows > 0 && (!make_kv_map(&maps.k, cfg, k, cfg->k_row_stride, cfg->k_head_stride, kStepKeys) ||
+                          !make_kv_map(&maps.v, cfg, v, cfg->v_row_stride, cfg->v_head_stride, kStepKeys)))
+    return fail(SVDQ_ERR_CUDA, "cuTensorMapEncodeTiled (keys or values) failed");
+  const cudaError_t e = launch_attention_step(p, maps, cfg->dtype == SVDQ_BF16, pl.sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("attention kernel: ") + cudaGetErrorString(e));
+  return SVDQ_OK;
+}
+
+svdq_status svdq_operator_status(void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  bool timeout = false;
+  for (auto take : {take_status_attention_step, take_status_dense}) {
+    int status = 0;
+    const cudaError_t e = take(&status, st);
+    if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("operator status: ") + cudaGetErrorString(e));
+    timeout |= status == kDevTimeout;
+  }
+  if (timeout) return fail(SVDQ_ERR_DEVICE_TIMEOUT, "a kernel gave up a pipeline wait");
+  return SVDQ_OK;
+}
+
+}  // extern "C"

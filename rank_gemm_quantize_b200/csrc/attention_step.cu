@@ -1,0 +1,519 @@
+// Attention of few queries per sequence (single new tokens, short pieces): the
+// keys and values are read once at memory speed, split over the SMs along the
+// sequence and joined by a second kernel.
+//
+// The query heads of a key head and the queries of a sequence form one list of
+// rows (row = query * group + head), cut into tiles of 16. A CTA of four warps
+// takes one item (16 rows, a share of the keys, one key head) after another.
+// TMA brings 64 keys and values at a time into a ring of stages; each warp
+// takes 16 of them: scores by mma.m16n8k16, softmax statistics and the product
+// with V in registers, with no exchange between warps until the item's end. The
+// shares' results (unnormalised float sums, maximum, sum) go to the workspace,
+// or straight to the output where a sequence has one share.
+//
+// Memory bounds it: 4 dim bytes a key and key head; 16 rows cost a fraction of
+// the tensor pipe, which is why the narrow mma is used here and a 128-row
+// tensor-memory tile would only add latency.
+#include <string>
+
+#include "attention.cuh"
+#include "operator_status.cuh"
+
+using namespace svdq;
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+
+template <int DP>
+struct StepSmem {
+  static constexpr int kTile = kStepKeys * DP * 2;  // keys, or values
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kStages = 96 * 1024 / kStage;  // 96 KB of loads: two CTAs an SM
+  static constexpr int kPitch = DP + 4;               // floats of a row when the warps' sums are joined
+  static constexpr int kBars = kStages * kStage;
+  static constexpr int kTotal = kBars + 1024 + 1024;
+  static_assert(kWarps * kStepRows * kPitch * 4 <= kStages * kStage, "the join reuses the stages");
+};
+
+// Row tiles, key shares and workspace slots of a sequence.
+struct Shares {
+  int tiles, chunks, slots;
+};
+__device__ __forceinline__ Shares shares_of(const AttnParams& p, int b) {
+  int qs, ql, ks, kl;
+  seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
+  seq_extent(p.k_offsets, b, p.k_rows, ks, kl);
+  Shares s;
+  s.tiles = (ql * p.group + kStepRows - 1) / kStepRows;
+  s.chunks = s.tiles <= kSplitTiles && kl > p.chunk ? (kl + p.chunk - 1) / p.chunk : 1;
+  s.slots = s.chunks > 1 ? s.tiles * s.chunks : 0;
+  return s;
+}
+
+__device__ __forceinline__ int warp_inclusive(int v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (static_cast<int>(lane_id()) >= o) v += u;
+  }
+  return v;
+}
+
+struct Found {
+  int b, tile, chunk, chunks, slot;
+};
+struct Search {  // where the search for an item stands: sequences before b0 hold `items` items and `slots` slots
+  int b0, items, slots;
+};
+
+// The sequence, row tile and key share of item `idx`: false behind the last.
+// Called by the whole CTA with idx that never decreases.
+__device__ bool find_item(const AttnParams& p, Search& at, int idx, Found* found, int (*sums)[2]) {
+  for (; at.b0 < p.batch; at.b0 += kThreads) {
+    const int b = at.b0 + static_cast<int>(threadIdx.x);
+    Shares s{0, 0, 0};
+    if (b < p.batch) s = shares_of(p, b);
+    const int own = s.tiles * s.chunks;
+    int items = warp_inclusive(own), slots = warp_inclusive(s.slots);
+    __syncthreads();  // the previous use of sums and found is over
+    if (lane_id() == 31) {
+      sums[warp_id()][0] = items;
+      sums[warp_id()][1] = slots;
+    }
+    __syncthreads();
+    int total_items = 0, total_slots = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == static_cast<int>(warp_id())) items += total_items, slots += total_slots;
+      total_items += sums[w][0];
+      total_slots += sums[w][1];
+    }
+    if (idx < at.items + total_items) {
+      const int first = at.items + items - own;
+      if (idx >= first && idx < first + own) {
+        const int i = idx - first;
+        found->b = b;
+        found->tile = i / s.chunks;
+        found->chunk = i % s.chunks;
+        found->chunks = s.chunks;
+        found->slot = at.slots + slots - s.slots + i;
+      }
+      __syncthreads();
+      return true;
+    }
+    at.items += total_items;
+    at.slots += total_slots;
+  }
+  return false;
+}
+
+__device__ __forceinline__ void ldsm(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <class T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (Half16<T>::kFmt == 1)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte piece `piece` of row `key` in a swizzled tile of 64
+// rows: columns of 64 values (128 bytes) side by side.
+__device__ __forceinline__ uint32_t tile_at(int key, int piece) {
+  return (piece >> 3) * (kStepKeys * 128) + key * 128 + (((piece & 7) ^ (key & 7)) << 4);
+}
+
+template <class T, int DP>
+__global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps) {
+  using L = StepSmem<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* empty = full + L::kStages;
+  __shared__ int sums[kWarps][2];
+  __shared__ Found found;
+  __shared__ int spoiled;
+  __shared__ int abort_word;
+  __shared__ float warp_ml[kWarps][kStepRows][2];
+  volatile int* abort_flag = &abort_word;
+
+  const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
+  const int g = lane >> 2, t = lane & 3;
+  const int hk = blockIdx.y;
+  if (tid == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWarps);
+    }
+    abort_word = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+
+  uint32_t used = 0;    // key tiles since the kernel's start
+  uint32_t issued = 0;  // ... and how many of them thread 0 has asked for
+  Search at{0, 0, 0};
+  for (int item = blockIdx.x;; item += gridDim.x) {
+    if (!find_item(p, at, item, &found, sums)) return;
+    const Found f = found;
+    int qs, ql, ks, kl;
+    seq_extent(p.q_offsets, f.b, p.q_rows, qs, ql);
+    seq_extent(p.k_offsets, f.b, p.k_rows, ks, kl);
+    const int rows = ql * p.group;
+    const int row0 = f.tile * kStepRows;
+    // keys [k_begin, k_end) of this share; row r sees keys <= limit(r)
+    const int k_begin = f.chunks > 1 ? f.chunk * p.chunk : 0;
+    auto limit = [&](int row) {
+      if (row >= rows) return -1;
+      return p.causal ? min(row / p.group + kl - ql, kl - 1) : kl - 1;
+    };
+    const int k_end = min(f.chunks > 1 ? k_begin + p.chunk : kl, limit(min(row0 + kStepRows, rows) - 1) + 1);
+    const int first_limit = limit(row0);
+    const int tiles = k_end > k_begin ? (k_end - k_begin + kStepKeys - 1) / kStepKeys : 0;
+
+    auto issue = [&](int i) {  // one thread: key tile i of this item
+      const int s = (used + i) % L::kStages;
+      uint8_t* st = smem + s * L::kStage;
+      mbar_arrive_expect_tx(&full[s], L::kStage);
+      const int key = ks + k_begin + i * kStepKeys;
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) {
+        tma_load_3d(st + c * kStepKeys * 128, &maps.k, &full[s], c * 64, hk, key);
+        tma_load_3d(st + L::kTile + c * kStepKeys * 128, &maps.v, &full[s], c * 64, hk, key);
+      }
+    };
+    if (tid == 0) {
+      spoiled = 0;
+      // every stage is free: the last item's tiles were all used
+      for (int i = 0; i < min(tiles, L::kStages); ++i) issue(i);
+    }
+    issued = used + min(tiles, L::kStages);
+
+    // the rows' queries as mma operands
+    uint32_t qf[DP / 16][4];
+    {
+      const T* qb = static_cast<const T*>(p.q);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = row0 + g + 8 * h;
+        const bool in = row < rows;
+        const T* src = qb + static_cast<long long>(qs + (in ? row / p.group : 0)) * p.q_row +
+                       (hk * p.group + (in ? row % p.group : 0)) * p.q_head;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int col = 16 * k + 8 * w + 2 * t;
+            qf[k][h + 2 * w] = in && col < p.dim ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
+          }
+      }
+    }
+    const int lim[2] = {limit(row0 + g), limit(row0 + g + 8)};
+    float o[DP / 8][4];
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    int i = 0;
+    for (; i < tiles; ++i) {
+      const uint32_t n = used + i;
+      const int s = n % L::kStages;
+      if (!mbar_wait(&full[s], (n / L::kStages) & 1, abort_flag, &g_status)) break;
+      uint8_t* st = smem + s * L::kStage;
+      const uint32_t kt = smem_u32(st), vt = kt + L::kTile;
+      const int key0 = k_begin + i * kStepKeys + 16 * warp;  // the warp's 16 keys
+      // Values of keys that no row sees, or not every row, must not meet the
+      // product (0 times infinity): keys behind the sequence become 0;
+      // infinities and NaN of the others become 0 here and are put back into
+      // the rows that do see them at the end.
+      if (key0 + 15 > first_limit) {
+        bool any = false;
+        for (int e = lane; e < 16 * (DP / 8); e += 32) {
+          const int r = e / (DP / 8), key = key0 + r;
+          if (key <= first_limit) continue;
+          uint4* at16 = reinterpret_cast<uint4*>(st + L::kTile + tile_at(16 * warp + r, e % (DP / 8)));
+          uint4 v = *at16;
+          if (key >= kl)
+            *at16 = make_uint4(0, 0, 0, 0);
+          else if (drop_non_finite<T>(v))
+            *at16 = v, any = true;
+        }
+        if (any) spoiled = 1;
+        fence_proxy_async_smem();  // the stage is loaded again by TMA
+        __syncwarp();
+      }
+      float sc[2][4];
+#pragma unroll
+      for (int a = 0; a < 2; ++a) sc[a][0] = sc[a][1] = sc[a][2] = sc[a][3] = 0.f;
+      {
+        const int mtx = lane >> 3, key = 16 * warp + (mtx >> 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          uint32_t b[4];
+          ldsm(kt + tile_at(key, 2 * k + (mtx & 1)), b);
+          mma16816<T>(sc[0], qf[k], b[0], b[1]);
+          mma16816<T>(sc[1], qf[k], b[2], b[3]);
+        }
+      }
+      float corr[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float top = m[h];
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = sc[a][2 * h + e];
+            if (key0 + 8 * a + 2 * t + e > lim[h]) x = -INFINITY;
+            top = fmaxf(top, x);
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float base = (top == -INFINITY ? 0.f : top) * p.scale_log2;
+        corr[h] = exp2_fast(fmaf(m[h], p.scale_log2, -base));
+        m[h] = top;
+        float sum = 0.f;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = sc[a][2 * h + e];
+            x = exp2_fast(fmaf(x, p.scale_log2, -base));
+            sum += x;
+          }
+        l[h] = fmaf(l[h], corr[h], sum);
+      }
+#pragma unroll
+      for (int n8 = 0; n8 < DP / 8; ++n8) {
+        o[n8][0] *= corr[0];
+        o[n8][1] *= corr[0];
+        o[n8][2] *= corr[1];
+        o[n8][3] *= corr[1];
+      }
+      const uint32_t pf[4] = {Half16<T>::pack(sc[0][0], sc[0][1]), Half16<T>::pack(sc[0][2], sc[0][3]),
+                              Half16<T>::pack(sc[1][0], sc[1][1]), Half16<T>::pack(sc[1][2], sc[1][3])};
+      {
+        const int mtx = lane >> 3, key = 16 * warp + (mtx & 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          uint32_t b[4];
+          ldsm_t(vt + tile_at(key, 2 * k + (mtx >> 1)), b);
+          mma16816<T>(o[2 * k], pf, b[0], b[1]);
+          mma16816<T>(o[2 * k + 1], pf, b[2], b[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+      if (tid == 0 && i + L::kStages < tiles && mbar_wait(&empty[s], (n / L::kStages) & 1, abort_flag, &g_status)) {
+        issue(i + L::kStages);
+        ++issued;
+      }
+    }
+    __syncwarp();
+    // the row sums over the four threads of a row
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
+    __syncthreads();  // every warp is done with the stages
+    if (*abort_flag) {  // a wait gave up: let the copies in flight land, then leave
+      if (tid == 0) {
+        volatile int no_abort = 0;
+        for (uint32_t n = issued > L::kStages ? issued - L::kStages : 0; n < issued; ++n)
+          mbar_wait(&full[n % L::kStages], (n / L::kStages) & 1, &no_abort, nullptr);
+      }
+      return;
+    }
+    used += tiles;
+    // join the warps: each row's maximum, sum and products
+    float* join = reinterpret_cast<float*>(smem);
+    if (t == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        warp_ml[warp][g + 8 * h][0] = m[h];
+        warp_ml[warp][g + 8 * h][1] = l[h];
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(join + (warp * kStepRows + g + 8 * h) * L::kPitch + 8 * n + 2 * t) =
+            make_float2(o[n][2 * h], o[n][2 * h + 1]);
+    __syncthreads();
+    const int r = tid >> 3, row = row0 + r;
+    if (row < rows) {
+      float top = -INFINITY, total = 0.f, w[kWarps];
+#pragma unroll
+      for (int a = 0; a < kWarps; ++a) top = fmaxf(top, warp_ml[a][r][0]);
+      const float base = (top == -INFINITY ? 0.f : top) * p.scale_log2;
+#pragma unroll
+      for (int a = 0; a < kWarps; ++a) {
+        w[a] = exp2_fast(fmaf(warp_ml[a][r][0], p.scale_log2, -base));
+        total = fmaf(warp_ml[a][r][1], w[a], total);
+      }
+      const bool split = f.chunks > 1;
+      const float norm = split || total == 0.f ? 1.f : 1.f / total;
+      const int row_limit = limit(row);
+      const size_t slot = (static_cast<size_t>(f.slot) * p.kv_heads + hk) * kStepRows + r;
+      const bool fits = f.slot < p.max_slots;
+#pragma unroll
+      for (int c0 = 0; c0 < DP; c0 += 32) {
+        const int c = c0 + (tid & 7) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int a = 0; a < kWarps; ++a) {
+          const float4 v = *reinterpret_cast<const float4*>(join + (a * kStepRows + r) * L::kPitch + c);
+          acc.x = fmaf(v.x, w[a], acc.x);
+          acc.y = fmaf(v.y, w[a], acc.y);
+          acc.z = fmaf(v.z, w[a], acc.z);
+          acc.w = fmaf(v.w, w[a], acc.w);
+        }
+        if (spoiled && c < p.dim) {
+          for (int key = max(k_begin, first_limit + 1); key < min(k_end, row_limit + 1); ++key) {
+            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.v) + static_cast<long long>(ks + key) * p.v_row +
+                                                            hk * p.v_head + c);
+            const uint32_t e[4] = {v.x & 0xFFFFu, v.x >> 16, v.y & 0xFFFFu, v.y >> 16};
+            float* x = &acc.x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if ((e[j] & Half16<T>::kExp) == Half16<T>::kExp) x[j] += Half16<T>::to_float(e[j]);
+          }
+        }
+        if (split) {
+          if (fits) *reinterpret_cast<float4*>(p.part + slot * DP + c) = acc;
+        } else if (c < p.dim) {
+          uint2 v;
+          v.x = Half16<T>::pack(acc.x * norm, acc.y * norm);
+          v.y = Half16<T>::pack(acc.z * norm, acc.w * norm);
+          *reinterpret_cast<uint2*>(static_cast<T*>(p.out) +
+                                    (static_cast<size_t>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim + c) = v;
+        }
+      }
+      if (split && fits && (tid & 7) == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, total);
+    }
+    fence_proxy_async_smem();  // the stages are loaded again by TMA
+    __syncthreads();
+  }
+}
+
+// Joins the shares: a row's softmax over all of them. CTA (b, key head, z)
+// takes rows z, z + gridDim.z, ..; its warps take every fourth share.
+template <class T, int DP>
+__global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnParams p) {
+  __shared__ int sums[kWarps];
+  __shared__ float warp_ml[kWarps][2];
+  __shared__ float warp_o[kWarps][DP];
+  const int b = blockIdx.x, hk = blockIdx.y, warp = warp_id(), lane = lane_id();
+  const Shares s = shares_of(p, b);
+  if (!s.slots) return;
+  int before = 0;
+  for (int j = threadIdx.x; j < b; j += kThreads) before += shares_of(p, j).slots;
+  before = __shfl_sync(0xffffffffu, warp_inclusive(before), 31);
+  if (lane == 0) sums[warp] = before;
+  __syncthreads();
+  before = sums[0] + sums[1] + sums[2] + sums[3];
+  if (before + s.slots > p.max_slots) return;
+  int qs, ql;
+  seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
+  constexpr int kPer = DP / 32;
+  for (int row = blockIdx.z; row < ql * p.group; row += gridDim.z) {
+    const int first = before + row / kStepRows * s.chunks;
+    float top = -INFINITY, total = 0.f, o[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int c = warp; c < s.chunks; c += kWarps) {
+      const size_t slot = (static_cast<size_t>(first + c) * p.kv_heads + hk) * kStepRows + row % kStepRows;
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot);
+      float v[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) v[e] = p.part[slot * DP + kPer * lane + e];
+      const float now = fmaxf(top, ml.x), base = (now == -INFINITY ? 0.f : now) * p.scale_log2;
+      const float was = exp2_fast(fmaf(top, p.scale_log2, -base)), w = exp2_fast(fmaf(ml.x, p.scale_log2, -base));
+      top = now;
+      total = fmaf(total, was, ml.y * w);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] = fmaf(o[e], was, v[e] * w);
+    }
+    if (lane == 0) {
+      warp_ml[warp][0] = top;
+      warp_ml[warp][1] = total;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) warp_o[warp][kPer * lane + e] = o[e];
+    __syncthreads();
+    if (threadIdx.x < DP / 2) {
+      const int c = 2 * threadIdx.x;
+      top = -INFINITY;
+#pragma unroll
+      for (int a = 0; a < kWarps; ++a) top = fmaxf(top, warp_ml[a][0]);
+      const float base = (top == -INFINITY ? 0.f : top) * p.scale_log2;
+      float x = 0.f, y = 0.f;
+      total = 0.f;
+#pragma unroll
+      for (int a = 0; a < kWarps; ++a) {
+        const float w = exp2_fast(fmaf(warp_ml[a][0], p.scale_log2, -base));
+        total = fmaf(warp_ml[a][1], w, total);
+        x = fmaf(warp_o[a][c], w, x);
+        y = fmaf(warp_o[a][c + 1], w, y);
+      }
+      const float norm = total == 0.f ? 1.f : 1.f / total;
+      if (c < p.dim)
+        *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) +
+                                     (static_cast<size_t>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim + c) =
+            Half16<T>::pack(x * norm, y * norm);
+    }
+    __syncthreads();
+  }
+}
+
+template <class T, int DP>
+cudaError_t start(const AttnParams& p, const AttnMaps& maps, int sms, cudaStream_t st) {
+  using L = StepSmem<DP>;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(attention_step_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+  });
+  if (e != cudaSuccess) return e;
+  // two CTAs an SM go through the items; no more of them than items
+  const long long rows = static_cast<long long>(p.q_rows) * p.group;
+  const long long items = p.max_slots + rows / kStepRows + p.batch;
+  const long long fill = (2ll * sms + p.kv_heads - 1) / p.kv_heads;
+  attention_step_kernel<T, DP><<<dim3(static_cast<unsigned>(std::min(items, fill)), p.kv_heads), kThreads, L::kTotal, st>>>(p, maps);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.max_slots == 0) return e;
+  const int z = static_cast<int>(std::min<long long>(kSplitTiles * kStepRows, (rows + p.batch - 1) / p.batch));
+  attention_join_kernel<T, DP><<<dim3(p.batch, p.kv_heads, z), kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+namespace svdq {
+
+cudaError_t take_status_attention_step(int* status, cudaStream_t st) { return take_status(status, st); }
+
+cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, int sms, cudaStream_t st) {
+  if (p.dim <= 64) return bf16 ? start<__nv_bfloat16, 64>(p, maps, sms, st) : start<__half, 64>(p, maps, sms, st);
+  return bf16 ? start<__nv_bfloat16, 128>(p, maps, sms, st) : start<__half, 128>(p, maps, sms, st);
+}
+
+}  // namespace svdq

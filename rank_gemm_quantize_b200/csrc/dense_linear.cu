@@ -1,0 +1,306 @@
+// The linear layer whose weight stays in 16 bits, with bias, activation and
+// residual in the product's epilogue:
+//   Y = residual + act(X W + bias),  X [M, K], W [K, N] (read in place)
+//
+// Rows kernel (few tiles): a CTA computes Y^T for 128 columns of W and RB
+// rows of X. W^T is the tensor core's A operand (the tile [64 k, 128 n] lands by
+// TMA as it lies in memory: M-major), X its B operand, so a product with few
+// rows costs few tensor-core columns and the kernel streams W at memory speed.
+// Where the tiles do not fill the SMs, the CTAs of a cluster take shares
+// of K: each sends its float partial sums of a slice of the rows to the CTA that
+// owns the slice (distributed shared memory), and the owner adds them in a
+// fixed order. No workspace, no atomics, one launch.
+#include <algorithm>
+#include <cstdint>
+#include <string>
+
+#include "attention.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "operator_status.cuh"
+
+namespace svdq {
+void set_last_error(const std::string& msg);
+}
+
+using namespace svdq;
+
+namespace {
+
+svdq_status fail(svdq_status st, const std::string& msg) {
+  set_last_error(msg);
+  return st;
+}
+
+struct DenseParams {
+  const void *bias, *residual;  // may be NULL
+  void* Y;
+  int M, N, K, act;
+};
+struct DenseMaps {
+  CUtensorMap x;  // X [M, K], box {64, rows of a tile}, 128-byte swizzle, zero fill
+  CUtensorMap w;  // W [K, N], box {64, 64}, 128-byte swizzle, zero fill
+};
+
+__device__ __forceinline__ float activate(float t, int act) {
+  switch (act) {
+    case SVDQ_ACT_RELU:
+      return t < 0.f ? 0.f : t;  // NaN stays
+    case SVDQ_ACT_SILU:
+      return __fdividef(t, 1.f + __expf(-t));
+    case SVDQ_ACT_GELU:
+      return 0.5f * t * erfcf(-0.70710678118654752f * t);
+    case SVDQ_ACT_GELU_TANH: {
+      // (1 + tanh(z)) / 2 = 1 / (1 + exp(-2 z))
+      const float z = 0.79788456080286536f * fmaf(0.044715f * t * t, t, t);
+      return __fdividef(t, 1.f + __expf(-2.f * z));
+    }
+    default:
+      return t;
+  }
+}
+
+// Eight columns of a row: bias, activation, residual, one rounding.
+template <class T>
+__device__ __forceinline__ void finish8(const DenseParams& p, int m, int n, float (&v)[8]) {
+  if (p.bias) {
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + n));
+    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] += Half16<T>::to_float(w[e] & 0xFFFFu);
+      v[2 * e + 1] += Half16<T>::to_float(w[e] >> 16);
+    }
+  }
+  if (p.act != SVDQ_ACT_NONE) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = activate(v[e], p.act);
+  }
+  const size_t at = static_cast<size_t>(m) * p.N + n;
+  if (p.residual) {
+    const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.residual) + at);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] += Half16<T>::to_float(w[e] & 0xFFFFu);
+      v[2 * e + 1] += Half16<T>::to_float(w[e] >> 16);
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<T*>(p.Y) + at) =
+      make_uint4(Half16<T>::pack(v[0], v[1]), Half16<T>::pack(v[2], v[3]), Half16<T>::pack(v[4], v[5]), Half16<T>::pack(v[6], v[7]));
+}
+
+constexpr int kBK = 64;
+
+// ---------------------------------------------------------------- rows kernel
+constexpr int kRowsN = 128;  // columns of W of a CTA
+constexpr int kRowsThreads = 128;
+
+template <int RB>
+struct RowsSmem {
+  static constexpr int kW = kRowsN * kBK * 2;  // 16 KB
+  static constexpr int kX = RB * kBK * 2;
+  static constexpr int kStage = kW + kX;
+  static constexpr int kStages = RB == 128 ? 6 : 96 * 1024 / kStage;  // up to 64 rows: two CTAs an SM
+  static constexpr int kPitch = kRowsN + 4;  // floats of a row of partial sums
+  static constexpr int kBars = kStages * kStage;
+  static constexpr int kTotal = kBars + 256 + 1024;
+  static_assert(RB * kPitch * 4 <= kStages * kStage, "the partial sums reuse the stages");
+};
+
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t rank, float v) {
+  asm volatile(
+      "{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %0, %1;\n"
+      " st.shared::cluster.f32 [ra], %2;\n}\n" ::"r"(addr),
+      "r"(rank), "f"(v)
+      : "memory");
+}
+
+template <class T, int RB>
+__global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DenseParams p, const __grid_constant__ DenseMaps maps, int shares) {
+  using L = RowsSmem<RB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* acc_full = empty + L::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  constexpr uint32_t kCols = RB < 32 ? 32 : RB;
+
+  const int warp = warp_id(), lane = lane_id();
+  const int share = blockIdx.x % shares;  // also the rank in the cluster
+  const int n0 = blockIdx.x / shares * kRowsN;
+  const int m0 = blockIdx.y * RB;
+  const int blocks = (p.K + kBK - 1) / kBK;
+  const int first = static_cast<int>(static_cast<long long>(blocks) * share / shares);
+  const int last = static_cast<int>(static_cast<long long>(blocks) * (share + 1) / shares);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int i = first;
+      for (; i < last; ++i) {
+        const int n = i - first, s = n % L::kStages;
+        if (!mbar_wait(&empty[s], ((n / L::kStages) & 1) ^ 1, abort_flag, &g_status)) break;
+        uint8_t* st = smem + s * L::kStage;
+        mbar_arrive_expect_tx(&full[s], L::kStage);
+        tma_load_2d(st, &maps.w, &full[s], n0, i * kBK);
+        tma_load_2d(st + 8192, &maps.w, &full[s], n0 + 64, i * kBK);
+        tma_load_2d(st + L::kW, &maps.x, &full[s], i * kBK, m0);
+      }
+      if (i < last) {  // gave up: the copies in flight land before shared memory is used again
+        volatile int no_abort = 0;
+        for (int n = std::max(0, i - first - L::kStages); n < i - first; ++n)
+          mbar_wait(&full[n % L::kStages], (n / L::kStages) & 1, &no_abort, nullptr);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // A: W^T, 128 columns of W, M-major (bit 15); B: X, RB rows, K-major
+      const uint32_t idesc = idesc_dense(kFmtF32, Half16<T>::kFmt, Half16<T>::kFmt, kRowsN, RB) | (1u << 15);
+      for (int n = 0; n < last - first; ++n) {
+        const int s = n % L::kStages;
+        if (!mbar_wait(&full[s], (n / L::kStages) & 1, abort_flag, &g_status)) break;
+        tc_fence_after();
+        const uint32_t wa = smem_u32(smem + s * L::kStage), xb = wa + L::kW;
+#pragma unroll
+        for (int k = 0; k < kBK / 16; ++k)
+          mma_f16(tmem, smem_desc(wa + 2048 * k, 8192, 1024, kSw128), smem_desc(xb + 32 * k, 16, 1024, kSw128), idesc,
+                  (n > 0 || k > 0) ? 1u : 0u);
+        tc_commit(&empty[s]);
+      }
+      tc_commit(acc_full);
+    }
+    __syncwarp();
+  }
+  volatile int no_abort = 0;
+  mbar_wait(acc_full, 0, &no_abort, &g_status);
+  tc_fence_after();
+  if (shares > 1) cluster_sync_all();  // every CTA of the cluster is done with its stages
+  else __syncthreads();
+
+  // partial sums to the owners of the rows: [share][row of the slice][column]
+  const int slice = RB / shares;
+  const uint32_t recv = smem_u32(smem);
+#pragma unroll
+  for (int c = 0; c < RB; c += 8) {
+    uint32_t r[8];
+    tmem_ld8(tmem + (static_cast<uint32_t>(32 * warp) << 16) + c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int m = c + e, owner = m / slice;
+      const uint32_t at = recv + ((share * slice + m % slice) * L::kPitch + 32 * warp + lane) * 4;
+      if (m0 + m < p.M) store_cluster(at, owner, __uint_as_float(r[e]));
+    }
+  }
+  tc_fence_before();
+  if (shares > 1) cluster_sync_all();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+  const float* sums = reinterpret_cast<const float*>(smem);
+  for (int i = threadIdx.x; i < slice * (kRowsN / 8); i += kRowsThreads) {
+    const int r = i / (kRowsN / 8), c = i % (kRowsN / 8) * 8;
+    const int m = m0 + share * slice + r, n = n0 + c;
+    if (m >= p.M || n >= p.N) continue;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < shares; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(sums + (s * slice + r) * L::kPitch + c);
+      const float4 a = src[0], b = src[1];
+      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+      v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    }
+    finish8<T>(p, m, n, v);
+  }
+}
+
+template <class T, int RB>
+cudaError_t start_rows(const DenseParams& p, const DenseMaps& maps, int sms, cudaStream_t st) {
+  using L = RowsSmem<RB>;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(dense_rows_kernel<T, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+  });
+  if (e != cudaSuccess) return e;
+  const int tiles_n = (p.N + kRowsN - 1) / kRowsN, tiles_m = (p.M + RB - 1) / RB;
+  // shares of K while they find free SMs and keep four blocks of K each
+  const int room = (RB == 128 ? 1 : 2) * sms, blocks = (p.K + kBK - 1) / kBK;
+  int shares = 1;
+  while (shares < 8 && 2ll * shares * tiles_n * tiles_m <= room && blocks >= 8 * shares) shares *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(tiles_n * shares, tiles_m);
+  cfg.blockDim = dim3(kRowsThreads);
+  cfg.dynamicSmemBytes = L::kTotal;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = shares;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dense_rows_kernel<T, RB>, p, maps, shares);
+}
+
+template <class T>
+svdq_status run(const DenseParams& p, const void* X, const void* W, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return fail(SVDQ_ERR_CUDA, "no usable current device");
+  const CUtensorMapDataType dt = Half16<T>::kFmt == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const int rb = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  DenseMaps maps{};
+  if (!make_map(&maps.x, dt, X, p.K, p.M, static_cast<uint64_t>(p.K) * 2, kBK, rb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&maps.w, dt, W, p.N, p.K, static_cast<uint64_t>(p.N) * 2, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B))
+    return fail(SVDQ_ERR_CUDA, "cuTensorMapEncodeTiled (dense linear) failed");
+  const cudaError_t e = rb == 16   ? start_rows<T, 16>(p, maps, sms, st)
+                        : rb == 32 ? start_rows<T, 32>(p, maps, sms, st)
+                        : rb == 64 ? start_rows<T, 64>(p, maps, sms, st)
+                                   : start_rows<T, 128>(p, maps, sms, st);
+  if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("dense linear kernel: ") + cudaGetErrorString(e));
+  return SVDQ_OK;
+}
+
+}  // namespace
+
+namespace svdq {
+cudaError_t take_status_dense(int* status, cudaStream_t st) { return take_status(status, st); }
+}  // namespace svdq
+
+extern "C" svdq_status svdq_dense_linear_forward(int dtype, const void* X, const void* W, const void* bias, const void* residual,
+                                                 int activation, int M, int K, int N, void* Y, void* stream) {
+  if (dtype != SVDQ_BF16 && dtype != SVDQ_F16) return fail(SVDQ_ERR_INVALID_ARG, "unknown dtype");
+  if (activation < SVDQ_ACT_NONE || activation > SVDQ_ACT_GELU_TANH) return fail(SVDQ_ERR_INVALID_ARG, "unknown activation");
+  if (M < 0 || K <= 0 || N <= 0 || K % 8 || N % 8)
+    return fail(SVDQ_ERR_INVALID_ARG, "M must not be negative, K and N positive multiples of 8");
+  if (M > 1 << 22 || K > 1 << 22 || N > 1 << 22) return fail(SVDQ_ERR_UNSUPPORTED, "M, K or N exceeds 4194304");
+  if (M == 0) return SVDQ_OK;
+  if (!X || !W || !Y) return fail(SVDQ_ERR_INVALID_ARG, "X, W or Y is NULL");
+  uintptr_t bits = 0;
+  for (const void* q : {X, W, bias, residual, static_cast<const void*>(Y)}) bits |= reinterpret_cast<uintptr_t>(q);
+  if (bits & 15) return fail(SVDQ_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  const DenseParams p{bias, residual, Y, M, N, K, activation};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return dtype == SVDQ_BF16 ? run<__nv_bfloat16>(p, X, W, st) : run<__half>(p, X, W, st);
+}

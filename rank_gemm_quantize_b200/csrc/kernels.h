@@ -13,6 +13,9 @@ namespace svdq {
 // between rows), box {box_inner, box_outer}; false if encoding failed.
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
               uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+// A 3-D tiled TMA map: dims from the contiguous one outwards, strides in bytes of the outer two.
+bool make_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[3],
+                 const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle sw);
 
 // LoRA adapter slots a layer can hold at once (bit s of a row's adapter mask
 // selects slot s).

@@ -1,0 +1,224 @@
+"""Attention of packed sequences (svdq_attention_forward) against its definition in 64 bits."""
+import pytest
+import torch
+
+import operators as ops
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+def make(seed, q_lengths, k_lengths, heads, kv_heads, dim, dtype, spread=1.5):
+    g = torch.Generator().manual_seed(seed)
+    t = lambda n, h, s=1.0: (torch.randn(n, h, dim, generator=g) * s).to(dtype).cuda()
+    return t(sum(q_lengths), heads, spread), t(sum(k_lengths), kv_heads), t(sum(k_lengths), kv_heads)
+
+
+def offsets(lengths):
+    return torch.tensor([0] + list(lengths)).cumsum(0).to(torch.int32).cuda()
+
+
+def run(q, k, v, q_lengths, k_lengths, causal, **how):
+    import rank_gemm_quantize_b200 as rq
+    o = rq.attention(q, k, v, offsets(q_lengths), offsets(k_lengths), causal=causal, **how)
+    torch.cuda.synchronize()
+    assert rq.operator_status() == rq.Status.OK
+    return o
+
+
+def check(seed, q_lengths, k_lengths, heads, kv_heads, dim, dtype, causal, scale=None):
+    q, k, v = make(seed, q_lengths, k_lengths, heads, kv_heads, dim, dtype)
+    o = run(q, k, v, q_lengths, k_lengths, causal, scale=scale)
+    ops.check(o, *ops.attention(q, k, v, q_lengths, k_lengths, causal, scale))
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lengths", [[1], [2], [63], [64], [65], [127, 1, 129], [300, 0, 5, 257]])
+def test_prompts(lengths, causal):
+    check(1, lengths, lengths, 4, 2, 64, BF16, causal)
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (3, 1), (6, 2), (5, 5), (40, 1), (128, 1)])
+@pytest.mark.parametrize("lengths", [[70, 9], [1, 1, 1]])
+def test_groups(heads, kv_heads, lengths):
+    check(2, lengths, [n + 61 for n in lengths], heads, kv_heads, 64, BF16, True)
+
+
+@pytest.mark.parametrize("dim", [8, 24, 64, 72, 96, 120, 128])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("q_lengths", [[140], [1, 3]])
+def test_head_dims(dim, dtype, q_lengths):
+    check(3, q_lengths, [n + 90 for n in q_lengths], 4, 2, dim, dtype, True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("k_lengths", [[1], [64], [777], [5000, 1, 63, 2047], [0, 20, 0, 9000]])
+def test_single_tokens(k_lengths, dtype):
+    check(4, [1] * len(k_lengths), k_lengths, 8, 2, 128, dtype, True)
+
+
+@pytest.mark.parametrize("q_lengths,k_lengths", [([2, 8, 17], [4000, 100, 2500]), ([33], [9001]), ([70, 1], [3000, 8000])])
+@pytest.mark.parametrize("causal", [False, True])
+def test_pieces_of_long_sequences(q_lengths, k_lengths, causal):
+    check(5, q_lengths, k_lengths, 8, 2, 128, BF16, causal)
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 128), (F16, 64)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_long_prompts(dtype, dim, causal):
+    check(6, [1100, 513, 256], [1100, 700, 256], 4, 2, dim, dtype, causal)
+
+
+@pytest.mark.parametrize("q_lengths,k_lengths", [([5, 200], [2, 60]), ([3], [0]), ([300, 2], [1, 1])])
+def test_queries_that_see_no_key_give_zero(q_lengths, k_lengths):
+    q, k, v = make(7, q_lengths, k_lengths, 4, 2, 64, BF16)
+    o = run(q, k, v, q_lengths, k_lengths, True)
+    ops.check(o, *ops.attention(q, k, v, q_lengths, k_lengths, True))
+    at = 0
+    for n, m in zip(q_lengths, k_lengths):
+        assert not o[at:at + max(0, n - m)].count_nonzero()
+        at += n
+
+
+@pytest.mark.parametrize("q_lengths", [[1, 1, 1], [150, 300, 70], [20, 20, 20]])
+def test_what_a_query_does_not_see_does_not_reach_it(q_lengths):
+    """Infinities and NaN in the keys and values behind a query and in other sequences; a
+    sequence's own last key is seen by its last query, which gets what the definition gives."""
+    k_lengths = [n + 30 for n in q_lengths]
+    q, k, v = make(8, q_lengths, k_lengths, 4, 2, 64, BF16)
+    starts = [0, k_lengths[0], k_lengths[0] + k_lengths[1]]
+    k[starts[1]:starts[2]] = float("nan")  # the whole middle sequence
+    v[starts[1]:starts[2]] = float("inf")
+    v[starts[1] - 1, 0, 3] = float("inf")  # last value of the first one
+    v[starts[1] - 1, 1, 5] = float("nan")
+    v[-2, 1, 1] = float("-inf")
+    v[-1, 1, 2] = float("nan")
+    o = run(q, k, v, q_lengths, k_lengths, True)
+    a, b = q_lengths[0], q_lengths[0] + q_lengths[1]
+    assert o[a:b].isnan().all()
+    for rows, keys, n, m in ((slice(0, a), slice(0, starts[1]), q_lengths[0], k_lengths[0]),
+                             (slice(b, None), slice(starts[2], None), q_lengths[2], k_lengths[2])):
+        ops.check(o[rows], *ops.attention(q[rows], k[keys], v[keys], [n], [m], True))
+
+
+def test_large_scores_and_scales():
+    """Scores of hundreds: one key takes all; and a scale that makes all keys alike."""
+    q, k, v = make(9, [40, 1], [200, 900], 4, 2, 64, BF16, spread=40.0)
+    for scale in (None, 1e-6, 2.0):
+        o = run(q, k, v, [40, 1], [200, 900], True, scale=scale)
+        ops.check(o, *ops.attention(q, k, v, [40, 1], [200, 900], True, scale), what=f"scale {scale}")
+
+
+@pytest.mark.parametrize("lengths", [[300, 77], [1, 1, 1, 1]])
+def test_views_of_a_joint_projection(lengths):
+    """q, k and v as views of one [rows, (heads + 2 kv heads) dim] matrix, and a transposed layout."""
+    import rank_gemm_quantize_b200 as rq
+    heads, kv, dim, rows = 6, 2, 64, sum(lengths)
+    g = torch.Generator().manual_seed(10)
+    y = torch.randn(rows, (heads + 2 * kv) * dim, generator=g).to(BF16).cuda()
+    q, k, v = y.view(rows, heads + 2 * kv, dim).split([heads, kv, kv], 1)
+    want = ops.attention(q, k, v, lengths, lengths, True)
+    o = rq.attention(q, k, v, offsets(lengths), causal=True)
+    ops.check(o, *want)
+    turned = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v)]  # [heads, rows, dim] in memory
+    assert torch.equal(rq.attention(*turned, offsets(lengths), causal=True), o)
+
+
+def test_one_sequence_needs_no_offsets():
+    import rank_gemm_quantize_b200 as rq
+    q, k, v = make(11, [200], [200], 4, 2, 64, BF16)
+    assert torch.equal(rq.attention(q, k, v, causal=True), run(q, k, v, [200], [200], True))
+    assert torch.equal(rq.attention(q[:1], k, v), run(q[:1], k, v, [1], [200], False))
+
+
+@pytest.mark.parametrize("n", [1, 130])
+def test_rows_behind_the_last_sequence_stay(n):
+    import rank_gemm_quantize_b200 as rq
+    q, k, v = make(12, [n, n, n], [500, 20, 80], 4, 2, 64, BF16)
+    out = torch.full_like(q, 7.0)
+    o = rq.attention(q, k, v, offsets([n, n]), offsets([500, 20]), causal=True, out=out)
+    assert o is out and (out[2 * n:] == 7).all()
+    ops.check(out[:2 * n], *ops.attention(q[:2 * n], k[:520], v[:520], [n, n], [500, 20], True))
+
+
+@pytest.mark.parametrize("bad", [[0, 900, 300], [-5, 20, 1 << 30], [300, 200, 100], [-(1 << 31), (1 << 31) - 1, 7]])
+def test_bad_offsets_stay_inside_the_tensors(bad):
+    """Offsets that leave the tensors or run backwards give some result, and the next call is right."""
+    import rank_gemm_quantize_b200 as rq
+    for n in (2, 300):
+        q, k, v = make(13, [n], [600], 4, 2, 64, BF16)
+        o = torch.tensor(bad, dtype=torch.int32).cuda()
+        rq.attention(q, k, v, o, o, causal=True)
+        torch.cuda.synchronize()
+        assert rq.operator_status() == rq.Status.OK
+        ops.check(run(q, k, v, [n], [600], True), *ops.attention(q, k, v, [n], [600], True))
+
+
+@pytest.mark.parametrize("q_lengths,k_lengths", [([1] * 5, [700, 3000, 1, 64, 200]), ([400, 130], [400, 900])])
+def test_graph_stream_and_repetition(q_lengths, k_lengths):
+    """Captured and replayed on new inputs, on another stream, twice at once, and bit for bit alike."""
+    import rank_gemm_quantize_b200 as rq
+    q, k, v = make(14, q_lengths, k_lengths, 8, 2, 128, BF16)
+    qo, ko = offsets(q_lengths), offsets(k_lengths)
+    first = rq.attention(q, k, v, qo, ko, causal=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a = rq.attention(q, k, v, qo, ko, causal=True, stream=side)
+    b = rq.attention(q, k, v, qo, ko, causal=True)
+    torch.cuda.synchronize()
+    assert torch.equal(first, a) and torch.equal(first, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = rq.attention(q, k, v, qo, ko, causal=True)
+    q2, k2, v2 = make(15, q_lengths, k_lengths, 8, 2, 128, BF16)
+    for t, n in ((q, q2), (k, k2), (v, v2)):
+        t.copy_(n)
+    graph.replay()
+    torch.cuda.synchronize()
+    ops.check(captured, *ops.attention(q2, k2, v2, q_lengths, k_lengths, True))
+
+
+def test_given_workspace_and_its_check():
+    import rank_gemm_quantize_b200 as rq
+    q, k, v = make(16, [1, 1], [3000, 900], 4, 2, 64, BF16)
+    need = rq.attention_workspace_size(q, k, v, batch=2)
+    assert need > 0
+    qo, ko = offsets([1, 1]), offsets([3000, 900])
+    ws = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+    o = rq.attention(q, k, v, qo, ko, workspace=ws)
+    assert torch.equal(o, rq.attention(q, k, v, qo, ko))
+    assert (ws[need:] == 0xFF).all()
+    with pytest.raises(rq.SvdqError, match="workspace"):
+        rq.attention(q, k, v, qo, ko, workspace=ws[:256])
+
+
+def test_many_sequences():
+    """More sequences than threads of a CTA, most of them short or empty."""
+    g = torch.Generator().manual_seed(17)
+    k_lengths = torch.randint(0, 40, (700,), generator=g).tolist()
+    q_lengths = [min(1, n) for n in k_lengths]
+    k_lengths[13] = 2500
+    check(18, q_lengths, k_lengths, 2, 1, 64, BF16, True)
+
+
+def test_nothing_to_do():
+    import rank_gemm_quantize_b200 as rq
+    q, k, v = make(19, [0], [5], 4, 2, 64, BF16)
+    assert rq.attention(q, k, v).shape == (0, 4, 64)
+    q, k, v = make(20, [5], [0], 4, 2, 64, BF16)
+    assert not rq.attention(q, k, v).count_nonzero()
+
+
+def test_long_cache_passes_31_bits_of_offset():
+    """Keys whose byte offset passes 2^31 (values 2^32): a batch of two sequences, the second far out."""
+    import rank_gemm_quantize_b200 as rq
+    rows, kv, dim = 2_200_000, 8, 128
+    k = torch.zeros(rows, kv, dim, dtype=BF16, device="cuda")
+    v = torch.zeros_like(k)
+    q, kk, vv = make(21, [1, 1], [500, 700], 16, kv, dim, BF16)
+    k[:500], k[-700:], v[:500], v[-700:] = kk[:500], kk[500:], vv[:500], vv[500:]
+    # three sequences, the middle one without queries
+    o = rq.attention(q, k, v, torch.tensor([0, 1, 1, 2], dtype=torch.int32).cuda(),
+                     torch.tensor([0, 500, rows - 700, rows], dtype=torch.int32).cuda(), causal=True)
+    ops.check(o, *ops.attention(q, kk, vv, [1, 1], [500, 700], True))
