@@ -1,6 +1,7 @@
 // Host side of the attention calls: argument checks, tensor maps, the choice
 // of the kernel and of the shares the keys are cut into.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <string>
 
@@ -46,12 +47,14 @@ svdq_status check(const svdq_attention_config* c) {
 }
 
 struct Plan {
-  int sms, chunk, max_slots, padded;
-  size_t part, ml, total;
+  int sms, chunk, max_slots;
+  bool prompt;  // attention_prompt.cu, or attention_step.cu
+  size_t ml, total;
 };
 
-// The keys of few queries are cut into shares so that every SM has several of
-// them (two CTAs an SM, four shares a CTA).
+// Which kernel, and the shares the keys are cut into. The lengths of the
+// sequences are on the device: the rules go by the totals, and both kernels are
+// right for any lengths.
 svdq_status plan(const svdq_attention_config* c, Plan* out) {
   int dev = 0;
   Plan p{};
@@ -59,17 +62,28 @@ svdq_status plan(const svdq_attention_config* c, Plan* out) {
     cudaGetLastError();
     return fail(SVDQ_ERR_CUDA, "no usable current device");
   }
-  p.padded = c->head_dim <= 64 ? 64 : 128;
-  const long long shares = std::max<long long>(1, 8ll * p.sms / c->kv_heads);
-  const long long keys = (c->k_rows + shares - 1) / shares;
-  p.chunk = static_cast<int>(std::max<long long>(1, (keys + kStepKeys - 1) / kStepKeys) * kStepKeys);
-  // a sequence of more than `chunk` keys has fewer than 2 keys / chunk shares
   const long long rows = static_cast<long long>(c->q_rows) * (c->q_heads / c->kv_heads);
-  const int tiles = static_cast<int>(std::min<long long>(kSplitTiles, (rows + kStepRows - 1) / kStepRows));
-  p.max_slots = c->k_rows > p.chunk ? static_cast<int>(2ll * c->k_rows / p.chunk) * tiles : 0;
-  const size_t slot_rows = static_cast<size_t>(p.max_slots) * c->kv_heads * kStepRows;
-  p.part = 0;
-  p.ml = slot_rows * p.padded * 4;
+  p.prompt = rows > 64ll * c->batch;
+  const int key_tile = p.prompt ? kPromptKeys : kStepKeys, tile_rows = p.prompt ? kPromptRows : kStepRows;
+  long long keys, tiles;  // keys of a share; row tiles that can have several shares
+  if (p.prompt) {
+    // cut the keys only where the row tiles leave SMs idle, into no less than 512 of them
+    tiles = rows / kPromptRows + c->batch;
+    const long long shares = p.sms / (tiles * c->kv_heads);
+    keys = shares > 1 ? std::max<long long>(512, c->k_rows / shares) : c->k_rows;
+  } else {
+    // two CTAs an SM, four shares a CTA
+    tiles = std::min<long long>(kStepSplitTiles, (rows + kStepRows - 1) / kStepRows);
+    const long long shares = std::max<long long>(1, 8ll * p.sms / c->kv_heads);
+    keys = (c->k_rows + shares - 1) / shares;
+  }
+  p.chunk = static_cast<int>(std::max<long long>(1, (keys + key_tile - 1) / key_tile) * key_tile);
+  // a sequence of more than `chunk` keys has fewer than 2 keys / chunk shares
+  const long long slots = c->k_rows > p.chunk ? 2ll * c->k_rows / p.chunk * tiles : 0;
+  if ((slots + rows / tile_rows + c->batch) * c->kv_heads > 0x7fffffffll) return fail(SVDQ_ERR_UNSUPPORTED, "too many sequences times heads");
+  p.max_slots = static_cast<int>(slots);
+  const size_t slot_rows = static_cast<size_t>(slots) * c->kv_heads * tile_rows;
+  p.ml = slot_rows * (c->head_dim <= 64 ? 64 : 128) * 4;
   p.total = p.ml + slot_rows * 8;
   *out = p;
   return SVDQ_OK;
@@ -131,15 +145,21 @@ svdq_status svdq_attention_forward(const svdq_attention_config* cfg, const void*
   p.q_head = cfg->q_head_stride;
   p.v_row = cfg->v_row_stride;
   p.v_head = cfg->v_head_stride;
+  p.tile_rows = pl.prompt ? kPromptRows : kStepRows;
+  p.split_tiles = pl.prompt ? INT_MAX : kStepSplitTiles;
   p.chunk = pl.chunk;
   p.max_slots = pl.max_slots;
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.part);
+  p.part = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.ml);
   AttnMaps maps{};
-  if (cfg->k_rows > 0 && (!make_kv_map(&maps.k, cfg, k, cfg->k_row_stride, cfg->k_head_stride, kStepKeys) ||
-                          !make_kv_map(&maps.v, cfg, v, cfg->v_row_stride, cfg->v_head_stride, kStepKeys)))
+  const int key_tile = pl.prompt ? kPromptKeys : kStepKeys;
+  if (cfg->k_rows > 0 && (!make_kv_map(&maps.k, cfg, k, cfg->k_row_stride, cfg->k_head_stride, key_tile) ||
+                          !make_kv_map(&maps.v, cfg, v, cfg->v_row_stride, cfg->v_head_stride, key_tile)))
     return fail(SVDQ_ERR_CUDA, "cuTensorMapEncodeTiled (keys or values) failed");
-  const cudaError_t e = launch_attention_step(p, maps, cfg->dtype == SVDQ_BF16, pl.sms, static_cast<cudaStream_t>(stream));
+  const bool bf16 = cfg->dtype == SVDQ_BF16;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = pl.prompt ? launch_attention_prompt(p, maps, bf16, st) : launch_attention_step(p, maps, bf16, pl.sms, st);
+  if (e == cudaSuccess && pl.max_slots > 0) e = launch_attention_join(p, bf16, st);
   if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("attention kernel: ") + cudaGetErrorString(e));
   return SVDQ_OK;
 }
@@ -147,7 +167,7 @@ svdq_status svdq_attention_forward(const svdq_attention_config* cfg, const void*
 svdq_status svdq_operator_status(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   bool timeout = false;
-  for (auto take : {take_status_attention_step, take_status_dense}) {
+  for (auto take : {take_status_attention_step, take_status_attention_prompt, take_status_dense}) {
     int status = 0;
     const cudaError_t e = take(&status, st);
     if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("operator status: ") + cudaGetErrorString(e));

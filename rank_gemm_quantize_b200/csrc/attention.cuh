@@ -14,9 +14,11 @@ struct AttnParams {
   int batch, q_rows, k_rows, q_heads, kv_heads, group, dim, causal;
   float scale_log2;   // scale * log2(e): softmax in base 2
   long long q_row, q_head, v_row, v_head;  // strides in elements
-  // keys split over CTAs (few queries)
-  int chunk;          // keys of a share, a multiple of the key tile
-  int max_slots;      // partial results the workspace holds
+  // A sequence's rows (query * group + head in the group) are cut into tiles of
+  // tile_rows, its keys into shares of `chunk` (a multiple of the key tile) where
+  // it has at most split_tiles row tiles.
+  int tile_rows, split_tiles, chunk;
+  int max_slots;      // partial results (tile_rows rows each) the workspace holds
   float *part, *part_ml;
 };
 struct AttnMaps {
@@ -87,12 +89,94 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Keys and rows of the split kernel's tiles.
-constexpr int kStepKeys = 64;
-constexpr int kStepRows = 16;
-// Sequences of at most this many row tiles have their keys split over CTAs.
-constexpr int kSplitTiles = 4;
+// Row tiles, key shares and workspace slots of a sequence.
+struct Shares {
+  int tiles, chunks, slots;
+};
+__device__ __forceinline__ Shares shares_of(const AttnParams& p, int b) {
+  int qs, ql, ks, kl;
+  seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
+  seq_extent(p.k_offsets, b, p.k_rows, ks, kl);
+  Shares s;
+  s.tiles = (ql * p.group + p.tile_rows - 1) / p.tile_rows;
+  s.chunks = s.tiles <= p.split_tiles && kl > p.chunk ? (kl + p.chunk - 1) / p.chunk : 1;
+  s.slots = s.chunks > 1 ? s.tiles * s.chunks : 0;
+  return s;
+}
 
+__device__ __forceinline__ int warp_inclusive(int v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (static_cast<int>(lane_id()) >= o) v += u;
+  }
+  return v;
+}
+
+struct Found {
+  int b, tile, tiles, chunk, chunks;
+  int slots;  // workspace slots before the sequence's; it has slot tile * chunks + chunk of its own
+};
+struct Search {  // where the search for an item stands: sequences before b0 hold `items` items and `slots` slots
+  int b0, items, slots;
+};
+
+// The sequence, row tile and key share of item `idx`: false behind the last.
+// Called by the whole CTA of WARPS warps with idx that never decreases.
+template <int WARPS>
+__device__ bool find_item(const AttnParams& p, Search& at, int idx, Found* found, int (*sums)[2]) {
+  for (; at.b0 < p.batch; at.b0 += WARPS * 32) {
+    const int b = at.b0 + static_cast<int>(threadIdx.x);
+    Shares s{0, 0, 0};
+    if (b < p.batch) s = shares_of(p, b);
+    const int own = s.tiles * s.chunks;
+    int items = warp_inclusive(own), slots = warp_inclusive(s.slots);
+    __syncthreads();  // the previous use of sums and found is over
+    if (lane_id() == 31) {
+      sums[warp_id()][0] = items;
+      sums[warp_id()][1] = slots;
+    }
+    __syncthreads();
+    int total_items = 0, total_slots = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w == static_cast<int>(warp_id())) items += total_items, slots += total_slots;
+      total_items += sums[w][0];
+      total_slots += sums[w][1];
+    }
+    if (idx < at.items + total_items) {
+      const int first = at.items + items - own;
+      if (idx >= first && idx < first + own) {
+        const int i = idx - first;
+        found->b = b;
+        found->tile = i / s.chunks;
+        found->tiles = s.tiles;
+        found->chunk = i % s.chunks;
+        found->chunks = s.chunks;
+        found->slots = at.slots + slots - s.slots;
+      }
+      __syncthreads();
+      return true;
+    }
+    at.items += total_items;
+    at.slots += total_slots;
+  }
+  return false;
+}
+
+// Few queries (attention_step.cu): row and key tiles; sequences of at most
+// this many row tiles have their keys split.
+constexpr int kStepRows = 16;
+constexpr int kStepKeys = 64;
+constexpr int kStepSplitTiles = 4;
+// Many queries (attention_prompt.cu): rows of a CTA (two tensor-memory tiles), key tile.
+constexpr int kPromptRows = 256;
+constexpr int kPromptKeys = 128;
+
+cudaError_t take_status_attention_prompt(int* status, cudaStream_t st);
+cudaError_t launch_attention_prompt(const AttnParams& p, const AttnMaps& maps, bool bf16, cudaStream_t st);
+// Joins the shares of the sequences that have several (after either kernel).
+cudaError_t launch_attention_join(const AttnParams& p, bool bf16, cudaStream_t st);
 cudaError_t take_status_attention_step(int* status, cudaStream_t st);
 cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, int sms, cudaStream_t st);
 

@@ -1,0 +1,441 @@
+// Attention of many queries per sequence (whole prompts, long pieces) on the
+// tensor cores, scores and results in tensor memory.
+//
+// The query heads of a key head and the queries of a sequence form one list of
+// rows (row = query * group + head), so grouped heads fill the tiles and read
+// each key once. A CTA takes 256 rows of one key head: two tiles of 128
+// rows. Per tile of 128 keys
+//   S = Q K^T     (both operands in shared memory, S float in tensor memory)
+//   P = 2^(c S - c m), rounded to 16 bits over S in tensor memory
+//   O += P V      (P from tensor memory, V from shared memory as it lies there)
+// with m the row's running maximum and the row's sum kept in registers: one thread
+// owns a row, so neither needs an exchange. While the threads of one tile work on
+// their scores, the tensor core multiplies for the other tile.
+//
+// O is not rescaled whenever m grows, only when it grew by more than 2^8 since
+// the last time: P may then be up to 2^8 instead of 1, which costs no digits
+// (its relative rounding is the same), and the final division puts it right.
+//
+// Warps: 0-3 and 4-7 the softmax of the two tiles (224 registers a thread: a
+// whole row of scores), 8 issues the MMAs, 9 the TMA loads, 10 and 11 keep
+// values that a query must not see out of the product (below). K and V tiles
+// share one ring of stages in the order K0 V0 K1 V1 ..
+#include <string>
+
+#include "attention.cuh"
+#include "operator_status.cuh"
+
+using namespace svdq;
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTileRows = 128;
+constexpr int kRegsSoftmax = 224, kRegsOther = 56;  // registers a thread: 256 threads and 128
+constexpr float kGrow = 8.f;  // log2 of how far the maximum may grow before O is rescaled
+
+template <int DP>
+struct PromptSmem {
+  static constexpr int kQTile = kTileRows * DP * 2;
+  static constexpr int kStage = kPromptKeys * DP * 2;  // one K or V tile
+  static constexpr int kStages = DP == 128 ? 5 : 8;
+  static constexpr int kRing = 2 * kQTile;
+  static constexpr int kBars = kRing + kStages * kStage;
+  static constexpr int kTotal = kBars + 512 + 1024;
+};
+static_assert(PromptSmem<128>::kTotal <= 232448, "shared memory budget");
+
+// Byte offset of 16-byte piece `piece` of a row in a swizzled tile of 128 rows.
+__device__ __forceinline__ uint32_t tile_at(int row, int piece) {
+  return (piece >> 3) * (128 * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+}
+
+// D[tmem] (+)= A[tmem] B: A is 16-bit pairs, one row a lane, 8 columns a k-step of 16.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+      "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Tensor memory: scores (and, over them, probabilities) of the two tiles, then the two results.
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kScoreCol = 0, kResultCol = 256;
+
+template <class T, int DP>
+__global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps) {
+  using L = PromptSmem<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // [kStages] a K or V tile can be used
+  uint64_t* empty = full + L::kStages;                            // [kStages] the MMAs are done with it
+  uint64_t* s_full = empty + L::kStages;                          // [2] a tile's scores are complete
+  uint64_t* p_full = s_full + 2;                                  // [2] its probabilities are written, O is rescaled
+  uint64_t* o_full = p_full + 2;                                  // [2] its result is complete
+  uint64_t* dirty = o_full + 2;                                   // [kStages] a V tile with hidden keys has landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dirty + L::kStages);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* spoiled = abort_flag + 1;
+  __shared__ int sums[kThreads / 32][2];
+  __shared__ Found found;
+
+  const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
+  const int hk = blockIdx.x % p.kv_heads;  // heads side by side: the heaviest tiles of all of them start first
+  Search at{0, 0, 0};
+  if (!find_item<kThreads / 32>(p, at, blockIdx.x / p.kv_heads, &found, sums)) return;
+  const Found f = found;
+  int qs, ql, ks, kl;
+  seq_extent(p.q_offsets, f.b, p.q_rows, qs, ql);
+  seq_extent(p.k_offsets, f.b, p.k_rows, ks, kl);
+  const int rows = ql * p.group;
+  // the tiles that see most keys first
+  const int tile = f.tiles - 1 - f.tile, row0 = tile * kPromptRows;
+  const int k_begin = f.chunks > 1 ? f.chunk * p.chunk : 0;
+  auto limit = [&](int row) {  // the last key a row sees
+    return p.causal ? min(row / p.group + kl - ql, kl - 1) : kl - 1;
+  };
+  auto key_tiles = [&](int t) {
+    const int first = row0 + t * kTileRows, last = min(first + kTileRows, rows) - 1;
+    if (first >= rows) return 0;
+    const int end = min(f.chunks > 1 ? k_begin + p.chunk : kl, limit(last) + 1);
+    return end > k_begin ? (end - k_begin + kPromptKeys - 1) / kPromptKeys : 0;
+  };
+  const int n0 = key_tiles(0), n1 = key_tiles(1), n = max(n0, n1);
+  const int first_limit = limit(row0);
+  // key tiles from this one on hold keys that some row does not see
+  const int first_hidden = max(0, first_limit + 1 - k_begin) / kPromptKeys;
+  // parity of the barrier on which such a V tile lands; its stage is that of every kPeriod-th V tile
+  constexpr int kPeriod = L::kStages % 2 ? L::kStages : L::kStages / 2;
+  auto hidden_parity = [&](int j) { return static_cast<uint32_t>((j - first_hidden) / kPeriod & 1); };
+
+  if (tid == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 2);  // twice by the load warp, or once each by the two that clean the tile
+      mbar_init(&empty[s], 1);
+      mbar_init(&dirty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&o_full[t], 1);
+    }
+    *abort_flag = 0;
+    *spoiled = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  // the rows' queries, 16 bytes at a time; zeros behind the last row and column
+  for (int e = tid; e < kPromptRows * (DP / 8); e += kThreads) {
+    const int r = e / (DP / 8), c = e % (DP / 8), row = row0 + r;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < rows && 8 * c < p.dim)
+      v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + static_cast<long long>(qs + row / p.group) * p.q_row +
+                                          (hk * p.group + row % p.group) * p.q_head + 8 * c);
+    *reinterpret_cast<uint4*>(smem + (r / kTileRows) * L::kQTile + tile_at(r % kTileRows, c)) = v;
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 9) {
+      // ------------------------------------------------------------ loads
+      if (lane == 0) {
+        int i = 0;
+        auto hidden = [&](int i) { return (i & 1) && (i >> 1) >= first_hidden; };
+        for (; i < 2 * n; ++i) {  // K of key tile i / 2, then its V
+          const int s = i % L::kStages;
+          if (!mbar_wait(&empty[s], ((i / L::kStages) & 1) ^ 1, abort_flag, &g_status)) break;
+          uint8_t* st = smem + L::kRing + s * L::kStage;
+          const CUtensorMap* map = i & 1 ? &maps.v : &maps.k;
+          uint64_t* bar = hidden(i) ? &dirty[s] : &full[s];
+          if (!hidden(i)) mbar_arrive(&full[s]);
+          mbar_arrive_expect_tx(bar, L::kStage);
+#pragma unroll
+          for (int c = 0; c < DP / 64; ++c)
+            tma_load_3d(st + c * 128 * 128, map, bar, c * 64, hk, ks + k_begin + (i >> 1) * kPromptKeys);
+        }
+        if (i < 2 * n) {  // gave up: the copies in flight land before the CTA ends
+          volatile int no_abort = 0;
+          for (int e = max(0, i - L::kStages); e < i; ++e)
+            if (hidden(e))
+              mbar_wait(&dirty[e % L::kStages], hidden_parity(e >> 1), &no_abort, nullptr);
+            else
+              mbar_wait(&full[e % L::kStages], (e / L::kStages) & 1, &no_abort, nullptr);
+        }
+      }
+    } else if (warp == 8) {
+      // ------------------------------------------------------------ MMAs
+      if (lane == 0 && n > 0) {
+        constexpr uint32_t kFmt = Half16<T>::kFmt;
+        const uint32_t idesc_s = idesc_dense(kFmtF32, kFmt, kFmt, kTileRows, kPromptKeys);
+        const uint32_t idesc_o = idesc_dense(kFmtF32, kFmt, kFmt, kTileRows, DP) | (1u << 16);  // V: columns contiguous
+        const uint32_t q = smem_u32(smem), ring = q + L::kRing;
+        auto wait_full = [&](int i) { return mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1, abort_flag, &g_status); };
+        auto scores = [&](int t, int i) {
+          const uint32_t a = q + t * L::kQTile, b = ring + (i % L::kStages) * L::kStage;
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint32_t at16 = (k >> 2) * (128 * 128) + (k & 3) * 32;
+            mma_f16(tmem + kScoreCol + t * 128, smem_desc(a + at16, 16, 1024, kSw128), smem_desc(b + at16, 16, 1024, kSw128), idesc_s, k > 0);
+          }
+          tc_commit(&s_full[t]);
+        };
+        auto products = [&](int t, int i, bool first) {
+          const uint32_t b = ring + (i % L::kStages) * L::kStage;
+#pragma unroll
+          for (int k = 0; k < kPromptKeys / 16; ++k)
+            mma_f16_ts(tmem + kResultCol + t * DP, tmem + kScoreCol + t * 128 + 8 * k, smem_desc(b + 2048 * k, 128 * 128, 1024, kSw128),
+                       idesc_o, !first || k > 0);
+        };
+        bool ok = wait_full(0);
+        if (ok) {
+          tc_fence_after();
+          if (n0 > 0) scores(0, 0);
+          if (n1 > 0) scores(1, 0);
+          tc_commit(&empty[0]);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+          const int iv = 2 * j + 1, ik = 2 * j + 2;
+          ok = wait_full(iv);
+          if (ok && j + 1 < n) ok = wait_full(ik);
+          for (int t = 0; t < 2 && ok; ++t) {
+            const int nt = t ? n1 : n0;
+            if (j >= nt) continue;
+            ok = mbar_wait(&p_full[t], j & 1, abort_flag, &g_status);
+            if (!ok) break;
+            tc_fence_after();
+            products(t, iv, j == 0);
+            if (j + 1 < nt)
+              scores(t, ik);  // over P: MMAs of one thread run in order
+            else
+              tc_commit(&o_full[t]);
+          }
+          if (!ok) break;
+          tc_commit(&empty[iv % L::kStages]);
+          if (j + 1 < n) tc_commit(&empty[ik % L::kStages]);
+        }
+        if (!ok) {  // gave up: the MMAs in flight end before the CTA does
+          tc_commit(&o_full[0]);
+          tc_commit(&o_full[1]);
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ hidden values
+      // A key that a row does not see has probability 0, but 0 times infinity is
+      // NaN: in tiles that hold hidden keys, values behind the sequence become 0;
+      // infinities and NaN of other keys that not every row sees become 0 too,
+      // and are put back into the rows that do see them at the end.
+      for (int j = first_hidden; j < n; ++j) {
+        const int stage = (2 * j + 1) % L::kStages;
+        if (!mbar_wait(&dirty[stage], hidden_parity(j), abort_flag, &g_status)) break;
+        uint8_t* st = smem + L::kRing + stage * L::kStage;
+        const int key0 = k_begin + j * kPromptKeys;
+        bool any = false;
+        for (int e = (warp - 10) * 32 + lane; e < kPromptKeys * (DP / 8); e += 64) {
+          const int r = e / (DP / 8);
+          if (key0 + r <= first_limit) continue;
+          uint4* at16 = reinterpret_cast<uint4*>(st + tile_at(r, e % (DP / 8)));
+          uint4 v = *at16;
+          if (key0 + r >= kl)
+            *at16 = make_uint4(0, 0, 0, 0);
+          else if (drop_non_finite<T>(v))
+            *at16 = v, any = true;
+        }
+        if (any) *spoiled = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // -------------------------------------------------------------- softmax
+    const int t = warp >> 2, nt = t ? n1 : n0;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t scores = tmem + lanes + kScoreCol + t * 128, result = tmem + lanes + kResultCol + t * DP;
+    const int row = row0 + t * kTileRows + 32 * (warp & 3) + lane;
+    const int lim = row < rows ? limit(row) : -1;
+    const int warp_limit = limit(row - lane);  // its first row sees least
+    const float c = p.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < nt; ++j) {
+      ok = mbar_wait(&s_full[t], j & 1, abort_flag, &g_status);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tmem_ld32(scores + 32 * b, s[b]);
+      tmem_ld_wait();
+      const int key0 = k_begin + j * kPromptKeys;
+      if (key0 + kPromptKeys - 1 > warp_limit) {
+        const int seen = lim - key0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * b + e > seen) s[b][e] = 0xFF800000u;  // minus infinity
+      }
+      float top[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        top[b] = __uint_as_float(s[b][0]);
+#pragma unroll
+        for (int e = 1; e < 32; ++e) top[b] = fmaxf(top[b], __uint_as_float(s[b][e]));
+      }
+      const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      const bool grew = (now - m) * c > kGrow;  // also the first time; false while nothing was seen
+      if (__any_sync(0xffffffffu, grew)) {
+        const float factor = grew ? exp2_fast((m - now) * c) : 1.f;
+        if (grew) m = now;
+        l *= factor;
+        if (j > 0) {  // the last product is complete: these scores were issued after it
+#pragma unroll
+          for (int b = 0; b < DP; b += 32) {
+            uint32_t o[32];
+            tmem_ld32(result + b, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+            tmem_st32(result + b, o);
+          }
+        }
+      }
+      const float base = (m == -INFINITY ? 0.f : m) * c;
+      const float2 c2 = make_float2(c, c), base2 = make_float2(-base, -base);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float2 x = __ffma2_rn(make_float2(__uint_as_float(s[b][2 * e]), __uint_as_float(s[b][2 * e + 1])), c2, base2);
+          x.x = exp2_fast(x.x);
+          x.y = exp2_fast(x.y);
+          sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+          pk[e] = Half16<T>::pack(x.x, x.y);
+        }
+        tmem_st16(scores + 16 * b, pk);
+      }
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[t]);
+    }
+    if (nt > 0) {
+      volatile int no_abort = 0;
+      ok = mbar_wait(&o_full[t], 0, &no_abort, &g_status) && ok && !*abort_flag;
+      tc_fence_after();
+    }
+    // ---------------------------------------------------------------- result
+    if (ok) {
+      const bool split = f.chunks > 1;
+      const float norm = split || l == 0.f ? 1.f : 1.f / l;
+      const int share = f.slots + tile * f.chunks + f.chunk;
+      const size_t slot = (static_cast<size_t>(share) * p.kv_heads + hk) * kPromptRows + row - row0;
+      const bool write = row < rows && (!split || share < p.max_slots);
+      const int spoil_end = *spoiled ? min(lim + 1, k_begin + nt * kPromptKeys) : 0;
+      T* out = static_cast<T*>(p.out) + (static_cast<size_t>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim;
+#pragma unroll 1
+      for (int b = 0; b < DP; b += 32) {
+        uint32_t o[32];
+        if (nt > 0) {
+          tmem_ld32(result + b, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (!write) continue;
+        for (int key = max(k_begin, first_limit + 1); key < spoil_end; ++key) {
+          const T* v = static_cast<const T*>(p.v) + static_cast<long long>(ks + key) * p.v_row + hk * p.v_head + b;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t bits = b + e < p.dim ? reinterpret_cast<const uint16_t*>(v)[e] : 0u;
+            if ((bits & Half16<T>::kExp) == Half16<T>::kExp) o[e] = __float_as_uint(__uint_as_float(o[e]) + Half16<T>::to_float(bits));
+          }
+        }
+        if (split) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(p.part + slot * DP + b + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) w[h] = Half16<T>::pack(__uint_as_float(o[e + 2 * h]) * norm, __uint_as_float(o[e + 2 * h + 1]) * norm);
+            if (b + e < p.dim) *reinterpret_cast<uint4*>(out + b + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (split && write) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(m, l);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <class T, int DP>
+cudaError_t start(const AttnParams& p, const AttnMaps& maps, cudaStream_t st) {
+  using L = PromptSmem<DP>;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = once_per_device(done, [] {
+    // the softmax warps' registers come out of what the block starts with
+    cudaFuncAttributes a;
+    const cudaError_t r = cudaFuncGetAttributes(&a, attention_prompt_kernel<T, DP>);
+    if (r != cudaSuccess) return r;
+    if (a.numRegs * kThreads < kRegsSoftmax * 256 + kRegsOther * 128) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(attention_prompt_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+  });
+  if (e != cudaSuccess) return e;
+  // CTAs behind the last item leave at once
+  const long long items = p.max_slots + static_cast<long long>(p.q_rows) * p.group / kPromptRows + p.batch;
+  attention_prompt_kernel<T, DP><<<static_cast<unsigned>(items * p.kv_heads), kThreads, L::kTotal, st>>>(p, maps);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+namespace svdq {
+
+cudaError_t take_status_attention_prompt(int* status, cudaStream_t st) { return take_status(status, st); }
+
+cudaError_t launch_attention_prompt(const AttnParams& p, const AttnMaps& maps, bool bf16, cudaStream_t st) {
+  if (p.dim <= 64) return bf16 ? start<__nv_bfloat16, 64>(p, maps, st) : start<__half, 64>(p, maps, st);
+  return bf16 ? start<__nv_bfloat16, 128>(p, maps, st) : start<__half, 128>(p, maps, st);
+}
+
+}  // namespace svdq

@@ -37,78 +37,6 @@ struct StepSmem {
   static_assert(kWarps * kStepRows * kPitch * 4 <= kStages * kStage, "the join reuses the stages");
 };
 
-// Row tiles, key shares and workspace slots of a sequence.
-struct Shares {
-  int tiles, chunks, slots;
-};
-__device__ __forceinline__ Shares shares_of(const AttnParams& p, int b) {
-  int qs, ql, ks, kl;
-  seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
-  seq_extent(p.k_offsets, b, p.k_rows, ks, kl);
-  Shares s;
-  s.tiles = (ql * p.group + kStepRows - 1) / kStepRows;
-  s.chunks = s.tiles <= kSplitTiles && kl > p.chunk ? (kl + p.chunk - 1) / p.chunk : 1;
-  s.slots = s.chunks > 1 ? s.tiles * s.chunks : 0;
-  return s;
-}
-
-__device__ __forceinline__ int warp_inclusive(int v) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
-    if (static_cast<int>(lane_id()) >= o) v += u;
-  }
-  return v;
-}
-
-struct Found {
-  int b, tile, chunk, chunks, slot;
-};
-struct Search {  // where the search for an item stands: sequences before b0 hold `items` items and `slots` slots
-  int b0, items, slots;
-};
-
-// The sequence, row tile and key share of item `idx`: false behind the last.
-// Called by the whole CTA with idx that never decreases.
-__device__ bool find_item(const AttnParams& p, Search& at, int idx, Found* found, int (*sums)[2]) {
-  for (; at.b0 < p.batch; at.b0 += kThreads) {
-    const int b = at.b0 + static_cast<int>(threadIdx.x);
-    Shares s{0, 0, 0};
-    if (b < p.batch) s = shares_of(p, b);
-    const int own = s.tiles * s.chunks;
-    int items = warp_inclusive(own), slots = warp_inclusive(s.slots);
-    __syncthreads();  // the previous use of sums and found is over
-    if (lane_id() == 31) {
-      sums[warp_id()][0] = items;
-      sums[warp_id()][1] = slots;
-    }
-    __syncthreads();
-    int total_items = 0, total_slots = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == static_cast<int>(warp_id())) items += total_items, slots += total_slots;
-      total_items += sums[w][0];
-      total_slots += sums[w][1];
-    }
-    if (idx < at.items + total_items) {
-      const int first = at.items + items - own;
-      if (idx >= first && idx < first + own) {
-        const int i = idx - first;
-        found->b = b;
-        found->tile = i / s.chunks;
-        found->chunk = i % s.chunks;
-        found->chunks = s.chunks;
-        found->slot = at.slots + slots - s.slots + i;
-      }
-      __syncthreads();
-      return true;
-    }
-    at.items += total_items;
-    at.slots += total_slots;
-  }
-  return false;
-}
-
 __device__ __forceinline__ void ldsm(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -170,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
   uint32_t issued = 0;  // ... and how many of them thread 0 has asked for
   Search at{0, 0, 0};
   for (int item = blockIdx.x;; item += gridDim.x) {
-    if (!find_item(p, at, item, &found, sums)) return;
+    if (!find_item<kWarps>(p, at, item, &found, sums)) return;
     const Found f = found;
     int qs, ql, ks, kl;
     seq_extent(p.q_offsets, f.b, p.q_rows, qs, ql);
@@ -372,8 +300,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
       const bool split = f.chunks > 1;
       const float norm = split || total == 0.f ? 1.f : 1.f / total;
       const int row_limit = limit(row);
-      const size_t slot = (static_cast<size_t>(f.slot) * p.kv_heads + hk) * kStepRows + r;
-      const bool fits = f.slot < p.max_slots;
+      const int share = f.slots + f.tile * f.chunks + f.chunk;
+      const size_t slot = (static_cast<size_t>(share) * p.kv_heads + hk) * kStepRows + r;
+      const bool fits = share < p.max_slots;
 #pragma unroll
       for (int c0 = 0; c0 < DP; c0 += 32) {
         const int c = c0 + (tid & 7) * 4;
@@ -435,13 +364,13 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnPara
   seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
   constexpr int kPer = DP / 32;
   for (int row = blockIdx.z; row < ql * p.group; row += gridDim.z) {
-    const int first = before + row / kStepRows * s.chunks;
+    const int first = before + row / p.tile_rows * s.chunks, r = row % p.tile_rows;
     float top = -INFINITY, total = 0.f, o[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[e] = 0.f;
 #pragma unroll 4
     for (int c = warp; c < s.chunks; c += kWarps) {
-      const size_t slot = (static_cast<size_t>(first + c) * p.kv_heads + hk) * kStepRows + row % kStepRows;
+      const size_t slot = (static_cast<size_t>(first + c) * p.kv_heads + hk) * p.tile_rows + r;
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot);
       float v[kPer];
 #pragma unroll
@@ -498,10 +427,13 @@ cudaError_t start(const AttnParams& p, const AttnMaps& maps, int sms, cudaStream
   const long long items = p.max_slots + rows / kStepRows + p.batch;
   const long long fill = (2ll * sms + p.kv_heads - 1) / p.kv_heads;
   attention_step_kernel<T, DP><<<dim3(static_cast<unsigned>(std::min(items, fill)), p.kv_heads), kThreads, L::kTotal, st>>>(p, maps);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || p.max_slots == 0) return e;
-  const int z = static_cast<int>(std::min<long long>(kSplitTiles * kStepRows, (rows + p.batch - 1) / p.batch));
-  attention_join_kernel<T, DP><<<dim3(p.batch, p.kv_heads, z), kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <class T, int DP>
+cudaError_t join(const AttnParams& p, cudaStream_t st) {
+  const long long rows = (static_cast<long long>(p.q_rows) * p.group + p.batch - 1) / p.batch;
+  attention_join_kernel<T, DP><<<dim3(p.batch, p.kv_heads, static_cast<int>(std::min<long long>(rows, 4096))), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -514,6 +446,11 @@ cudaError_t take_status_attention_step(int* status, cudaStream_t st) { return ta
 cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, int sms, cudaStream_t st) {
   if (p.dim <= 64) return bf16 ? start<__nv_bfloat16, 64>(p, maps, sms, st) : start<__half, 64>(p, maps, sms, st);
   return bf16 ? start<__nv_bfloat16, 128>(p, maps, sms, st) : start<__half, 128>(p, maps, sms, st);
+}
+
+cudaError_t launch_attention_join(const AttnParams& p, bool bf16, cudaStream_t st) {
+  if (p.dim <= 64) return bf16 ? join<__nv_bfloat16, 64>(p, st) : join<__half, 64>(p, st);
+  return bf16 ? join<__nv_bfloat16, 128>(p, st) : join<__half, 128>(p, st);
 }
 
 }  // namespace svdq
