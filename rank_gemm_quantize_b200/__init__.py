@@ -9,6 +9,7 @@ importing this module without the built library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from enum import IntEnum
@@ -475,78 +476,78 @@ class MlpBlock:
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _ACTIVATION = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _NORM = {None: 0, "layer": 1, "rms": 2}
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _operand(name: str, t: torch.Tensor, dtype: torch.dtype, device: torch.device, *shape) -> int:
+def _place(t: torch.Tensor) -> int:
+    """The device of a call's first tensor."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    return device
+
+
+def _operand(name: str, t: torch.Tensor, dtype: torch.dtype, device: int, shape: tuple) -> int:
     """The address of a contiguous tensor of this type, place and shape."""
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}, "
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on cuda:{device}, "
                          f"got {t.dtype} {list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _offsets(name: str, t: torch.Tensor, device: torch.device) -> int:
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or t.shape[0] < 2 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 [sequences + 1] tensor on {device}")
+def _offsets(name: str, t: torch.Tensor, device: int) -> int:
+    if t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 1 or t.shape[0] < 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 [sequences + 1] tensor on cuda:{device}")
     return t.data_ptr()
 
 
-class _Call:
-    """The device and stream of a call that keeps no handle: the device of its
-    tensors is made current, and what the call allocates stays valid for the
-    stream it runs on."""
-
-    def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        self.device = t.device
-        current = torch.cuda.current_stream(t.device).cuda_stream
-        self.stream = current if stream is None else _stream(stream)
-        self._other = self.stream != current
-        self._guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
-
-    def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self._other:
-            t.record_stream(torch.cuda.ExternalStream(self.stream, self.device))
-        return t
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self
-
-    def __exit__(self, *error):
-        if self._guard is not None:
-            self._guard.__exit__(*error)
+def _call_stream(device: int, stream, *made: torch.Tensor) -> int:
+    """The stream of a call; what the call allocated stays valid for it."""
+    current = _raw_stream(device)
+    if stream is None:
+        return current
+    handle = _stream(stream)
+    if handle != current:
+        for t in made:
+            if t is not None:
+                t.record_stream(torch.cuda.ExternalStream(handle, device))
+    return handle
 
 
 def _attention_config(q, k, v, batch, causal, scale) -> _Attention:
-    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or q.shape[2] != k.shape[2]:
-        raise ValueError(f"q must be [rows, heads, dim], k and v [rows, heads, dim] alike, got {tuple(q.shape)}, "
-                         f"{tuple(k.shape)}, {tuple(v.shape)}")
-    if q.dtype not in (torch.bfloat16, torch.float16) or k.dtype != q.dtype or v.dtype != q.dtype:
+    shape, keys = q.shape, k.shape
+    if len(shape) != 3 or len(keys) != 3 or keys != v.shape or shape[2] != keys[2]:
+        raise ValueError(f"q must be [rows, heads, dim], k and v [rows, heads, dim] alike, got {tuple(shape)}, "
+                         f"{tuple(keys)}, {tuple(v.shape)}")
+    dtype, device = q.dtype, q.get_device()
+    if dtype not in (torch.bfloat16, torch.float16) or k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError("q, k and v must all be bfloat16 or all float16")
-    if k.device != q.device or v.device != q.device:
+    if k.get_device() != device or v.get_device() != device:
         raise ValueError("q, k and v must be on one device")
-    c = _Attention(_DTYPE[q.dtype], batch, q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2], int(bool(causal)),
-                   q.shape[2] ** -0.5 if scale is None else scale)
-    for n, t in (("q", q), ("k", k), ("v", v)):
-        row, head, one = t.stride()
-        if one != 1 and t.shape[2] > 1:
-            raise ValueError(f"the values of a head of {n} must be contiguous")
-        setattr(c, n + "_row_stride", row)
-        setattr(c, n + "_head_stride", head)
-    return c
+    (qr, qh, q1), (kr, kh, k1), (vr, vh, v1) = q.stride(), k.stride(), v.stride()
+    if q1 != 1 or k1 != 1 or v1 != 1:
+        raise ValueError("the values of a head of q, k and v must be contiguous")
+    rows, heads, dim = shape
+    return _Attention(_DTYPE[dtype], batch, rows, keys[0], heads, keys[1], dim, 1 if causal else 0,
+                      dim ** -0.5 if scale is None else scale, qr, qh, kr, kh, vr, vh)
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_need(device: int, *shape: int) -> int:
+    """svdq_attention_workspace_size, which goes by the device and the shapes alone."""
+    dtype, batch, q_rows, k_rows, q_heads, kv_heads, dim = shape
+    n = ctypes.c_size_t()
+    _check(lib().svdq_attention_workspace_size(
+        ctypes.byref(_Attention(*shape, 0, 1.0, q_heads * dim, dim, kv_heads * dim, dim, kv_heads * dim, dim)), ctypes.byref(n)))
+    return n.value
 
 
 def attention_workspace_size(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, batch: int = 1) -> int:
     """Bytes of workspace attention() needs for these shapes."""
-    n = ctypes.c_size_t()
-    with _Call(q, None):
-        _check(lib().svdq_attention_workspace_size(ctypes.byref(_attention_config(q, k, v, batch, False, None)),
-                                                   ctypes.byref(n)))
-    return n.value
+    device = _place(q)
+    with torch.cuda.device(device):
+        c = _attention_config(q, k, v, batch, False, None)
+        return _attention_need(device, c.dtype, batch, c.q_rows, c.k_rows, c.q_heads, c.kv_heads, c.head_dim)
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Optional[torch.Tensor] = None,
@@ -563,34 +564,38 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opti
     sequence sees every key, the one before it all but one, and so on. scale
     defaults to dim ** -0.5. Rows of `out` that belong to no sequence are not
     written."""
-    with _Call(q, stream) as call:
-        if q_offsets is None:
-            if k_offsets is not None:
-                raise ValueError("k_offsets need q_offsets")
-            batch, qo, ko = 1, None, None
+    device = _place(q)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return attention(q, k, v, q_offsets, k_offsets, causal, scale, out, workspace, stream)
+    if q_offsets is None:
+        if k_offsets is not None:
+            raise ValueError("k_offsets need q_offsets")
+        batch, qo, ko = 1, None, None
+    else:
+        qo, batch = _offsets("q_offsets", q_offsets, device), q_offsets.shape[0] - 1
+        if k_offsets is None:
+            if q.shape[0] != k.shape[0]:
+                raise ValueError("k has other rows than q: k_offsets are needed")
+            ko = qo
         else:
-            qo = _offsets("q_offsets", q_offsets, q.device)
-            if k_offsets is None:
-                if q.shape[0] != k.shape[0]:
-                    raise ValueError("k has other rows than q: k_offsets are needed")
-                ko = qo
-            else:
-                ko = _offsets("k_offsets", k_offsets, q.device)
-                if k_offsets.shape != q_offsets.shape:
-                    raise ValueError("q_offsets and k_offsets must be of the same length")
-            batch = q_offsets.shape[0] - 1
-        cfg = _attention_config(q, k, v, batch, causal, scale)
-        need = ctypes.c_size_t()
-        _check(lib().svdq_attention_workspace_size(ctypes.byref(cfg), ctypes.byref(need)))
-        if out is None:
-            out = call.empty(q.shape, q.dtype)
-        o = _operand("out", out, q.dtype, q.device, *q.shape)
-        if workspace is None:
-            workspace = call.empty(need.value, torch.uint8)
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != q.device:
-            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-        _check(lib().svdq_attention_forward(ctypes.byref(cfg), q.data_ptr(), k.data_ptr(), v.data_ptr(), qo, ko, o,
-                                            workspace.data_ptr(), workspace.numel(), call.stream))
+            ko = _offsets("k_offsets", k_offsets, device)
+            if k_offsets.shape[0] != batch + 1:
+                raise ValueError("q_offsets and k_offsets must be of the same length")
+    cfg = _attention_config(q, k, v, batch, causal, scale)
+    need = _attention_need(device, cfg.dtype, batch, cfg.q_rows, cfg.k_rows, cfg.q_heads, cfg.kv_heads, cfg.head_dim)
+    made_out = made_workspace = None
+    if out is None:
+        out = made_out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(tuple(q.shape))
+    o = _operand("out", out, q.dtype, device, q.shape)
+    if workspace is None:
+        if need:
+            workspace = made_workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != device:
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _check(lib().svdq_attention_forward(ctypes.byref(cfg), q.data_ptr(), k.data_ptr(), v.data_ptr(), qo, ko, o, ws, size,
+                                        _call_stream(device, stream, made_out, made_workspace)))
     return out
 
 
@@ -600,21 +605,26 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     (include/svdq.h, svdq_dense_linear_forward): X [M, K], W [K, N], bias [N],
     residual and out [M, N], all bfloat16 or all float16; activation None, "relu",
     "silu", "gelu" or "gelu_tanh". out may be the residual."""
-    if X.dim() != 2 or W.dim() != 2 or X.dtype not in (torch.bfloat16, torch.float16):
+    dtype = X.dtype
+    if X.dim() != 2 or W.dim() != 2 or dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("X and W must be bfloat16 or float16 matrices")
-    if activation not in _ACTIVATION:
+    act = _ACTIVATION.get(activation)
+    if act is None:
         raise ValueError(f"unknown activation {activation!r}")
-    with _Call(X, stream) as call:
-        (M, K), N = X.shape, W.shape[1]
-        x = _operand("X", X, X.dtype, X.device, M, K)
-        w = _operand("W", W, X.dtype, X.device, K, N)
-        b = None if bias is None else _operand("bias", bias, X.dtype, X.device, N)
-        r = None if residual is None else _operand("residual", residual, X.dtype, X.device, M, N)
-        if out is None:
-            out = call.empty((M, N), X.dtype)
-        y = _operand("out", out, X.dtype, X.device, M, N)
-        _check(lib().svdq_dense_linear_forward(_DTYPE[X.dtype], x, w, b, r, _ACTIVATION[activation], M, K, N, y,
-                                               call.stream))
+    device = _place(X)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return linear(X, W, bias, activation, residual, out, stream)
+    (M, K), N = X.shape, W.shape[1]
+    x = _operand("X", X, dtype, device, (M, K))
+    w = _operand("W", W, dtype, device, (K, N))
+    b = None if bias is None else _operand("bias", bias, dtype, device, (N,))
+    r = None if residual is None else _operand("residual", residual, dtype, device, (M, N))
+    made = None
+    if out is None:
+        out = made = X.new_empty((M, N))
+    y = _operand("out", out, dtype, device, (M, N))
+    _check(lib().svdq_dense_linear_forward(_DTYPE[dtype], x, w, b, r, act, M, K, N, y, _call_stream(device, stream, made)))
     return out
 
 
@@ -642,39 +652,47 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
         raise ValueError("x must be a [rows, dim] tensor of bfloat16, float16 or float32")
     if norm not in _NORM or post_norm not in _NORM:
         raise ValueError(f"unknown norm {norm if norm not in _NORM else post_norm!r}")
-    rows, dim = x.shape
     kind = y.dtype if y is not None else dtype if dtype is not None else x.dtype
     if kind not in (torch.bfloat16, torch.float16) or x.dtype not in (kind, torch.float32):
         raise ValueError("y and h must be bfloat16 or float16, x of the same type or float32")
     if dtype is not None and dtype != kind:
         raise ValueError("dtype must be that of y")
-    with _Call(x, stream) as call:
-        a = _ResidualNorm(_DTYPE[kind], _DTYPE[x.dtype], rows, dim, 1, _NORM[post_norm], _NORM[norm], residual_scale, eps)
-        a.x = _operand("x", x, x.dtype, x.device, rows, dim)
-        if offsets is not None:
-            a.offsets = _offsets("offsets", offsets, x.device)
-            a.seqs = offsets.shape[0] - 1
-        for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("weight", weight), ("bias", bias)):
-            if t is not None:
-                setattr(a, name, _operand(name, t, kind, x.device, dim))
-        for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-            if t is not None:
-                shape = (dim,) if t.dim() == 1 and a.seqs == 1 else (a.seqs, dim)
-                setattr(a, name, _operand(name, t, kind, x.device, *shape))
-        if y is not None:
-            a.y = _operand("y", y, kind, x.device, rows, dim)
-            if out_x is None:
-                out_x = call.empty((rows, dim), x.dtype)
-            a.x_out = _operand("out_x", out_x, x.dtype, x.device, rows, dim)
-        elif out_x is not None:
-            raise ValueError("without y there is no out_x")
-        if norm is not None:
-            if out_h is None:
-                out_h = call.empty((rows, dim), kind)
-            a.h_out = _operand("out_h", out_h, kind, x.device, rows, dim)
-        elif out_h is not None:
-            raise ValueError("without a norm there is no out_h")
-        _check(lib().svdq_residual_norm(ctypes.byref(a), call.stream))
+    device = _place(x)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return residual_norm(x, y, offsets=offsets, gate=gate, residual_scale=residual_scale, post_norm=post_norm,
+                                 post_weight=post_weight, post_bias=post_bias, norm=norm, weight=weight, bias=bias,
+                                 scale=scale, shift=shift, eps=eps, dtype=dtype, out_x=out_x, out_h=out_h, stream=stream)
+    shape = x.shape
+    rows, dim = shape
+    seqs, off, made_x, made_h = 1, None, None, None
+    if offsets is not None:
+        off, seqs = _offsets("offsets", offsets, device), offsets.shape[0] - 1
+
+    def vector(name, t):
+        return None if t is None else _operand(name, t, kind, device, (dim,))
+
+    def row_of_sequence(name, t):
+        return None if t is None else _operand(name, t, kind, device, (dim,) if seqs == 1 and t.dim() == 1 else (seqs, dim))
+
+    if y is not None:
+        if out_x is None:
+            out_x = made_x = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out_x is not None:
+        raise ValueError("without y there is no out_x")
+    if norm is not None:
+        if out_h is None:
+            out_h = made_h = torch.empty_like(x if y is None else y, dtype=kind, memory_format=torch.contiguous_format)
+    elif out_h is not None:
+        raise ValueError("without a norm there is no out_h")
+    args = _ResidualNorm(
+        _DTYPE[kind], _DTYPE[x.dtype], rows, dim, seqs, _NORM[post_norm], _NORM[norm], residual_scale, eps,
+        _operand("x", x, x.dtype, device, shape), None if y is None else _operand("y", y, kind, device, shape),
+        None if y is None else _operand("out_x", out_x, x.dtype, device, shape),
+        None if norm is None else _operand("out_h", out_h, kind, device, shape),
+        row_of_sequence("gate", gate), vector("post_weight", post_weight), vector("post_bias", post_bias),
+        vector("weight", weight), vector("bias", bias), row_of_sequence("scale", scale), row_of_sequence("shift", shift), off)
+    _check(lib().svdq_residual_norm(ctypes.byref(args), _call_stream(device, stream, made_x, made_h)))
     return x if y is None else out_x, out_h
 
 

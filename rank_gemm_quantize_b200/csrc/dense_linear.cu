@@ -10,6 +10,11 @@
 // of K: each sends its float partial sums of a slice of the rows to the CTA that
 // owns the slice (distributed shared memory), and the owner adds them in a
 // fixed order. No workspace, no atomics, one launch.
+//
+// Pair kernel (many tiles): two SMs work as one (tcgen05 .cta_group::2) on a
+// 256 x 256 tile, each holding its own 128 rows of X and 128 columns of W.
+// Persistent; two accumulators in tensor memory, so the epilogue of a tile
+// runs under the next tile's products.
 #include <algorithm>
 #include <cstdint>
 #include <string>
@@ -40,6 +45,7 @@ struct DenseParams {
 struct DenseMaps {
   CUtensorMap x;  // X [M, K], box {64, rows of a tile}, 128-byte swizzle, zero fill
   CUtensorMap w;  // W [K, N], box {64, 64}, 128-byte swizzle, zero fill
+  CUtensorMap y;  // pair kernel: Y [M, N], box {32, 32}, 64-byte swizzle
 };
 
 __device__ __forceinline__ float activate(float t, int act) {
@@ -60,9 +66,9 @@ __device__ __forceinline__ float activate(float t, int act) {
   }
 }
 
-// Eight columns of a row: bias, activation, residual, one rounding.
+// Eight columns from n on of a row: bias, activation, residual, one rounding.
 template <class T>
-__device__ __forceinline__ void finish8(const DenseParams& p, int m, int n, float (&v)[8]) {
+__device__ __forceinline__ uint4 finish8(const DenseParams& p, int n, float (&v)[8], const uint4* residual) {
   if (p.bias) {
     const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + n));
     const uint32_t w[4] = {b.x, b.y, b.z, b.w};
@@ -76,18 +82,15 @@ __device__ __forceinline__ void finish8(const DenseParams& p, int m, int n, floa
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = activate(v[e], p.act);
   }
-  const size_t at = static_cast<size_t>(m) * p.N + n;
-  if (p.residual) {
-    const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.residual) + at);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  if (residual) {
+    const uint32_t w[4] = {residual->x, residual->y, residual->z, residual->w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       v[2 * e] += Half16<T>::to_float(w[e] & 0xFFFFu);
       v[2 * e + 1] += Half16<T>::to_float(w[e] >> 16);
     }
   }
-  *reinterpret_cast<uint4*>(static_cast<T*>(p.Y) + at) =
-      make_uint4(Half16<T>::pack(v[0], v[1]), Half16<T>::pack(v[2], v[3]), Half16<T>::pack(v[4], v[5]), Half16<T>::pack(v[6], v[7]));
+  return make_uint4(Half16<T>::pack(v[0], v[1]), Half16<T>::pack(v[2], v[3]), Half16<T>::pack(v[4], v[5]), Half16<T>::pack(v[6], v[7]));
 }
 
 constexpr int kBK = 64;
@@ -232,7 +235,10 @@ __global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DensePar
       v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
       v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
-    finish8<T>(p, m, n, v);
+    const size_t at = static_cast<size_t>(m) * p.N + n;
+    uint4 res;
+    if (p.residual) res = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.residual) + at);
+    *reinterpret_cast<uint4*>(static_cast<T*>(p.Y) + at) = finish8<T>(p, n, v, p.residual ? &res : nullptr);
   }
 }
 
@@ -263,18 +269,235 @@ cudaError_t start_rows(const DenseParams& p, const DenseMaps& maps, int sms, cud
   return cudaLaunchKernelEx(&cfg, dense_rows_kernel<T, RB>, p, maps, shares);
 }
 
+// ---------------------------------------------------------------- pair kernel
+constexpr int kPairM = 256, kPairN = 256;  // tile of a pair of SMs
+constexpr int kEpiWarps = 8;               // two per quarter of the lanes, 128 columns each
+constexpr int kPairThreads = (2 + kEpiWarps) * 32;
+constexpr int kGroupM = 16;                // row blocks that share the column blocks of W in L2
+
+struct PairSmem {
+  static constexpr int kX = 128 * kBK * 2;  // this CTA's rows
+  static constexpr int kW = kBK * 128 * 2;  // this CTA's columns
+  static constexpr int kStage = kX + kW;
+  static constexpr int kStages = 6;
+  static constexpr int kBox = 32 * 64;      // Y on its way out: 32 rows, 32 columns
+  static constexpr int kBoxes = kStages * kStage;
+  static constexpr int kBars = kBoxes + kEpiWarps * 2 * kBox;
+  static constexpr int kTotal = kBars + 512 + 1024;
+};
+static_assert(PairSmem::kTotal <= 232448, "shared memory budget");
+
+__device__ __forceinline__ void pair_tile(int tile, int m_blocks, int n_blocks, int& mb, int& nb) {
+  const int group = tile / (kGroupM * n_blocks), first = group * kGroupM, in = tile % (kGroupM * n_blocks);
+  const int size = min(kGroupM, m_blocks - first);
+  mb = first + in % size;
+  nb = in / size;
+}
+
+template <class T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    dense_pair_kernel(const DenseParams p, const __grid_constant__ DenseMaps maps) {
+  using L = PairSmem;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // [kStages] (leader) both CTAs' loads have landed
+  uint64_t* empty = full + L::kStages;                            // [kStages] (both) the MMAs are done with the stage
+  uint64_t* acc_full = empty + L::kStages;                        // [2] (both) a tile's sums are complete
+  uint64_t* acc_empty = acc_full + 2;                             // [2] (leader) both CTAs have read them
+  uint64_t* drain = acc_empty + 2;                                // (both) every MMA has completed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = warp_id(), lane = lane_id();
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int m_blocks = (p.M + kPairM - 1) / kPairM, n_blocks = (p.N + kPairN - 1) / kPairN;
+  const int tiles = m_blocks * n_blocks, pairs = gridDim.x >> 1;
+  const int blocks = (p.K + kBK - 1) / kBK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- loads (both CTAs)
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t it = 0;
+      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs) {
+        int mb, nb;
+        pair_tile(tile, m_blocks, n_blocks, mb, nb);
+        const int m = mb * kPairM + static_cast<int>(rank) * 128, n = nb * kPairN + static_cast<int>(rank) * 128;
+        for (int k = 0; k < blocks; ++k, ++it) {
+          const int s = it % L::kStages;
+          ok = mbar_wait(&empty[s], ((it / L::kStages) & 1) ^ 1, abort_flag, &g_status);
+          if (!ok) break;
+          uint8_t* st = smem + s * L::kStage;
+          const uint32_t bar = leader_addr(&full[s]);
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
+          tma_load_2d_pair(st, &maps.x, bar, k * kBK, m);
+          tma_load_2d_pair(st + L::kX, &maps.w, bar, n, k * kBK);
+          tma_load_2d_pair(st + L::kX + 8192, &maps.w, bar, n + 64, k * kBK);
+        }
+      }
+      if (!ok && leader) {  // gave up: the pair's copies in flight land before it ends
+        volatile int no_abort = 0;
+        for (uint32_t e = it > L::kStages ? it - L::kStages : 0; e < it; ++e)
+          mbar_wait(&full[e % L::kStages], (e / L::kStages) & 1, &no_abort, nullptr);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMAs (leader)
+    if (leader && lane == 0) {
+      // B: W, 256 columns over the pair, N-major (bit 16)
+      const uint32_t idesc = idesc_dense(kFmtF32, Half16<T>::kFmt, Half16<T>::kFmt, kPairM, kPairN) | (1u << 16);
+      bool ok = true;
+      uint32_t it = 0;
+      int ti = 0;
+      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs, ++ti) {
+        const int b = ti & 1;
+        ok = mbar_wait(&acc_empty[b], ((ti >> 1) & 1) ^ 1, abort_flag, &g_status);
+        if (!ok) break;
+        tc_fence_after();
+        for (int k = 0; k < blocks; ++k, ++it) {
+          const int s = it % L::kStages;
+          ok = mbar_wait(&full[s], (it / L::kStages) & 1, abort_flag, &g_status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t xa = smem_u32(smem + s * L::kStage), wb = xa + L::kX;
+#pragma unroll
+          for (int e = 0; e < kBK / 16; ++e)
+            mma_f16_pair(tmem + b * kPairN, smem_desc(xa + 32 * e, 16, 1024, kSw128), smem_desc(wb + 2048 * e, 8192, 1024, kSw128),
+                         idesc, (k > 0 || e > 0) ? 1u : 0u);
+          tc_commit_pair_mc(&empty[s], 0x3);
+        }
+        if (ok) tc_commit_pair_mc(&acc_full[b], 0x3);
+      }
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- epilogue (both CTAs)
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* box = smem + L::kBoxes + (warp - 2) * 2 * L::kBox;
+    const T* residual = static_cast<const T*>(p.residual);
+    int ti = 0;
+    for (int tile = blockIdx.x >> 1; tile < tiles; tile += pairs, ++ti) {
+      int mb, nb;
+      pair_tile(tile, m_blocks, n_blocks, mb, nb);
+      const int b = ti & 1, row0 = mb * kPairM + static_cast<int>(rank) * 128 + 32 * q, row = row0 + lane;
+      const int col0 = nb * kPairN + half * 128;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16) + b * kPairN + half * 128;
+      uint4 r4[4];  // the residual of the next 32 columns
+      auto fetch = [&](int c) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int n = col0 + c + 8 * v;
+          if (residual && row < p.M && n < p.N) r4[v] = *reinterpret_cast<const uint4*>(residual + static_cast<size_t>(row) * p.N + n);
+        }
+      };
+      fetch(0);
+      if (!mbar_wait(&acc_full[b], (ti >> 1) & 1, abort_flag, &g_status)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t a[32];
+        tmem_ld32(acc + c, a);
+        uint4 r[4] = {r4[0], r4[1], r4[2], r4[3]};
+        if (c + 32 < 128) fetch(c + 32);
+        tmem_ld_wait();
+        if (c + 32 == 128) {  // the sums are in registers: the next tile but one may start
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(&acc_empty[b], 0);
+        }
+        uint8_t* out = box + ((c >> 5) & 1) * L::kBox + lane * 64;
+        if (lane == 0) bulk_wait_group_read<1>();  // the store before the last has read this box
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int n = col0 + c + 8 * v;
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(a[8 * v + e]);
+          const uint4 y = n < p.N ? finish8<T>(p, n, x, residual ? &r[v] : nullptr) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(out + ((v ^ ((lane >> 1) & 3)) << 4)) = y;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (row0 < p.M && col0 + c < p.N) tma_store_2d(&maps.y, box + ((c >> 5) & 1) * L::kBox, col0 + c, row0);
+          bulk_commit_group();  // an empty one too: the waits above count groups
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  }
+
+  // Neither CTA leaves, or frees its tensor memory, while the other can still be
+  // signalled or read by the pair's MMAs.
+  if (warp == 1 && leader && lane == 0) tc_commit_pair_mc(drain, 0x3);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    volatile int no_abort = 0;
+    mbar_wait(drain, 0, &no_abort, nullptr);
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <class T>
+cudaError_t start_pair(const DenseParams& p, const DenseMaps& maps, int sms, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(dense_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairSmem::kTotal);
+  });
+  if (e != cudaSuccess) return e;
+  const long long tiles = static_cast<long long>((p.M + kPairM - 1) / kPairM) * ((p.N + kPairN - 1) / kPairN);
+  dense_pair_kernel<T><<<2 * static_cast<int>(std::min<long long>(tiles, sms / 2)), kPairThreads, PairSmem::kTotal, st>>>(p, maps);
+  return cudaGetLastError();
+}
+
 template <class T>
 svdq_status run(const DenseParams& p, const void* X, const void* W, cudaStream_t st) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return fail(SVDQ_ERR_CUDA, "no usable current device");
   const CUtensorMapDataType dt = Half16<T>::kFmt == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const int rb = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  const long long tiles = static_cast<long long>((p.M + kPairM - 1) / kPairM) * ((p.N + kPairN - 1) / kPairN);
+  const bool pair = p.M > 128 && tiles >= 32;
+  const int rb = pair ? 128 : p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
   DenseMaps maps{};
   if (!make_map(&maps.x, dt, X, p.K, p.M, static_cast<uint64_t>(p.K) * 2, kBK, rb, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&maps.w, dt, W, p.N, p.K, static_cast<uint64_t>(p.N) * 2, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B))
+      !make_map(&maps.w, dt, W, p.N, p.K, static_cast<uint64_t>(p.N) * 2, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (pair && !make_map(&maps.y, dt, p.Y, p.N, p.M, static_cast<uint64_t>(p.N) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
     return fail(SVDQ_ERR_CUDA, "cuTensorMapEncodeTiled (dense linear) failed");
-  const cudaError_t e = rb == 16   ? start_rows<T, 16>(p, maps, sms, st)
+  const cudaError_t e = pair       ? start_pair<T>(p, maps, sms, st)
+                        : rb == 16 ? start_rows<T, 16>(p, maps, sms, st)
                         : rb == 32 ? start_rows<T, 32>(p, maps, sms, st)
                         : rb == 64 ? start_rows<T, 64>(p, maps, sms, st)
                                    : start_rows<T, 128>(p, maps, sms, st);
