@@ -48,49 +48,74 @@ struct DenseMaps {
   CUtensorMap y;  // pair kernel: Y [M, N], box {32, 32}, 64-byte swizzle
 };
 
-__device__ __forceinline__ float activate(float t, int act) {
+// GELU of two values, t Phi(t) = t / (1 + 2^-g(t)) with g = log2(Phi(t) / Phi(-t)):
+// this form keeps the digits of the negative side, where 1 + erf loses them.
+// g(t) / t is even and smooth; P is a polynomial in t^2 fitted to it on [0, 30] by
+// weighted minimax (Lawson's iteration), the weight making the result's error at
+// most 2^-21 + 2^-18 |t Phi(t)| over 7. Behind the fit's end, where -t Phi(t)
+// < 2e-7, t^2 stays at 30. Seven packed multiply-adds, one ex2, one division.
+__device__ __forceinline__ float2 gelu2(float2 t) {
+  const float2 t2 = __fmul2_rn(t, t);
+  const float2 s = make_float2(fminf(t2.x, 30.f), fminf(t2.y, 30.f));
+  auto both = [](float c) { return make_float2(c, c); };
+  float2 q = both(5.11132959e-09f);
+  q = __ffma2_rn(q, s, both(-3.80040715e-07f));
+  q = __ffma2_rn(q, s, both(1.13597776e-05f));
+  q = __ffma2_rn(q, s, both(-0.000158607879f));
+  q = __ffma2_rn(q, s, both(-9.8645113e-05f));
+  q = __ffma2_rn(q, s, both(0.104843492f));
+  q = __ffma2_rn(q, s, both(2.30220498f));
+  const float2 g = __fmul2_rn(q, t);
+  return make_float2(__fdividef(t.x, 1.f + exp2_fast(-g.x)), __fdividef(t.y, 1.f + exp2_fast(-g.y)));
+}
+
+__device__ __forceinline__ float2 activate(float2 t, int act) {
   switch (act) {
     case SVDQ_ACT_RELU:
-      return t < 0.f ? 0.f : t;  // NaN stays
+      return make_float2(t.x < 0.f ? 0.f : t.x, t.y < 0.f ? 0.f : t.y);  // NaN stays
     case SVDQ_ACT_SILU:
-      return __fdividef(t, 1.f + __expf(-t));
+      return make_float2(__fdividef(t.x, 1.f + __expf(-t.x)), __fdividef(t.y, 1.f + __expf(-t.y)));
     case SVDQ_ACT_GELU:
-      return 0.5f * t * erfcf(-0.70710678118654752f * t);
+      return gelu2(t);
     case SVDQ_ACT_GELU_TANH: {
-      // (1 + tanh(z)) / 2 = 1 / (1 + exp(-2 z))
-      const float z = 0.79788456080286536f * fmaf(0.044715f * t * t, t, t);
-      return __fdividef(t, 1.f + __expf(-2.f * z));
+      // (1 + tanh(z)) / 2 = 1 / (1 + exp(-2 z)); 2 log2(e) sqrt(2 / pi) = 2.302208198
+      const float2 t2 = __fmul2_rn(t, t);
+      const float2 z = __fmul2_rn(__ffma2_rn(t2, make_float2(0.10294324f, 0.10294324f), make_float2(2.3022082f, 2.3022082f)), t);
+      return make_float2(__fdividef(t.x, 1.f + exp2_fast(-z.x)), __fdividef(t.y, 1.f + exp2_fast(-z.y)));
     }
     default:
       return t;
   }
 }
 
-// Eight columns from n on of a row: bias, activation, residual, one rounding.
 template <class T>
-__device__ __forceinline__ uint4 finish8(const DenseParams& p, int n, float (&v)[8], const uint4* residual) {
+__device__ __forceinline__ float2 unpack(uint32_t w) {
+  return make_float2(Half16<T>::to_float(w & 0xFFFFu), Half16<T>::to_float(w >> 16));
+}
+
+// Eight columns from n on of a row: bias, activation, residual (if p has one), one rounding.
+template <class T>
+__device__ __forceinline__ uint4 finish8(const DenseParams& p, int n, const float (&a)[8], const uint4& residual) {
+  float2 v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = make_float2(a[2 * e], a[2 * e + 1]);
   if (p.bias) {
     const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + n));
     const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] += Half16<T>::to_float(w[e] & 0xFFFFu);
-      v[2 * e + 1] += Half16<T>::to_float(w[e] >> 16);
-    }
+    for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(v[e], unpack<T>(w[e]));
   }
   if (p.act != SVDQ_ACT_NONE) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = activate(v[e], p.act);
+    for (int e = 0; e < 4; ++e) v[e] = activate(v[e], p.act);
   }
-  if (residual) {
-    const uint32_t w[4] = {residual->x, residual->y, residual->z, residual->w};
+  if (p.residual) {
+    const uint32_t w[4] = {residual.x, residual.y, residual.z, residual.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] += Half16<T>::to_float(w[e] & 0xFFFFu);
-      v[2 * e + 1] += Half16<T>::to_float(w[e] >> 16);
-    }
+    for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(v[e], unpack<T>(w[e]));
   }
-  return make_uint4(Half16<T>::pack(v[0], v[1]), Half16<T>::pack(v[2], v[3]), Half16<T>::pack(v[4], v[5]), Half16<T>::pack(v[6], v[7]));
+  return make_uint4(Half16<T>::pack(v[0].x, v[0].y), Half16<T>::pack(v[1].x, v[1].y), Half16<T>::pack(v[2].x, v[2].y),
+                    Half16<T>::pack(v[3].x, v[3].y));
 }
 
 constexpr int kBK = 64;
@@ -236,9 +261,9 @@ __global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DensePar
       v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
     const size_t at = static_cast<size_t>(m) * p.N + n;
-    uint4 res;
+    uint4 res = make_uint4(0, 0, 0, 0);
     if (p.residual) res = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.residual) + at);
-    *reinterpret_cast<uint4*>(static_cast<T*>(p.Y) + at) = finish8<T>(p, n, v, p.residual ? &res : nullptr);
+    *reinterpret_cast<uint4*>(static_cast<T*>(p.Y) + at) = finish8<T>(p, n, v, res);
   }
 }
 
@@ -406,12 +431,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int b = ti & 1, row0 = mb * kPairM + static_cast<int>(rank) * 128 + 32 * q, row = row0 + lane;
       const int col0 = nb * kPairN + half * 128;
       const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16) + b * kPairN + half * 128;
-      uint4 r4[4];  // the residual of the next 32 columns
+      uint4 r4[4] = {};  // the residual of the next 32 columns
       auto fetch = [&](int c) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int n = col0 + c + 8 * v;
-          if (residual && row < p.M && n < p.N) r4[v] = *reinterpret_cast<const uint4*>(residual + static_cast<size_t>(row) * p.N + n);
+          if (residual && row < p.M && n < p.N) r4[v] = __ldcs(reinterpret_cast<const uint4*>(residual + static_cast<size_t>(row) * p.N + n));
         }
       };
       fetch(0);
@@ -438,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           float x[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(a[8 * v + e]);
-          const uint4 y = n < p.N ? finish8<T>(p, n, x, residual ? &r[v] : nullptr) : make_uint4(0, 0, 0, 0);
+          const uint4 y = n < p.N ? finish8<T>(p, n, x, r[v]) : make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4*>(out + ((v ^ ((lane >> 1) & 3)) << 4)) = y;
         }
         fence_proxy_async_smem();

@@ -7,8 +7,14 @@
 // written once, and h is computed from the unrounded float x'.
 //
 // Both statistics are centred sums taken over values that stay in registers
-// (the mean first, then the squares of the differences), so a large mean
-// costs no digits. Memory bounds the kernel: (2 sizeof(x) + 4) bytes a value.
+// (the mean first, then the squares of the differences), so a large mean costs
+// no digits. Memory bounds a call of many rows: 2 (sizeof(x) + 2) bytes a value.
+// What decides how near it comes is how many rows an SM has under way, so the
+// layouts below keep the registers low and the blocks small (at 16384 x 4096 with
+// a float stream, norms on both sides, gate, scale and shift: 133 us, 92% of a copy's
+// rate; the vectors asked for earlier, with twice the registers: 152 us; a
+// persistent kernel fed by bulk copies through shared memory: 187 to 348 us). A call
+// of few rows takes one row's latency, 2.6 us.
 #include <algorithm>
 #include <cstdint>
 #include <string>
@@ -57,36 +63,76 @@ __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat
 template <>
 __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 
-// VEC consecutive values, as wide loads where VEC is 8.
+// VEC consecutive values as they lie in memory: words of 16, 4 or 2 bytes.
+template <int BYTES>
+struct WordOf;
+template <>
+struct WordOf<16> {
+  using type = uint4;
+};
+template <>
+struct WordOf<8> {
+  using type = uint2;
+};
+template <>
+struct WordOf<4> {
+  using type = uint32_t;
+};
+template <>
+struct WordOf<2> {
+  using type = uint16_t;
+};
 template <class T, int VEC>
-__device__ __forceinline__ void load(const void* base, size_t at, float (&v)[VEC]) {
-  const T* p = static_cast<const T*>(base) + at;
-  if constexpr (VEC == 8) {
-    constexpr int kWords = sizeof(T) / 2;
-    uint4 w[kWords];
+struct Raw {
+  static constexpr int kWord = VEC * sizeof(T) < 16 ? VEC * sizeof(T) : 16;
+  static constexpr int kWords = VEC * sizeof(T) / kWord;
+  typename WordOf<kWord>::type w[kWords];
+  __device__ __forceinline__ void load(const void* base, size_t at) {  // never an output of the call
+    const auto* p = reinterpret_cast<const typename WordOf<kWord>::type*>(static_cast<const T*>(base) + at);
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
-    const T* t = reinterpret_cast<const T*>(w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f(t[i]);
-  } else {
-    v[0] = to_f(p[0]);
+    for (int i = 0; i < kWords; ++i) w[i] = __ldg(p + i);
   }
+  __device__ __forceinline__ void load_once(const void* base, size_t at) {  // read by no other row
+    const auto* p = reinterpret_cast<const typename WordOf<kWord>::type*>(static_cast<const T*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __ldcs(p + i);
+  }
+  __device__ __forceinline__ void store(void* base, size_t at) const {
+    auto* p = reinterpret_cast<typename WordOf<kWord>::type*>(static_cast<T*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) p[i] = w[i];
+  }
+  __device__ __forceinline__ float get(int e) const { return to_f(reinterpret_cast<const T*>(w)[e]); }
+  __device__ __forceinline__ void set(int e, float v) { reinterpret_cast<T*>(w)[e] = from_f<T>(v); }
+};
+
+// a *= b, a += b, a = s b + a on VEC values, two at a time.
+template <int VEC>
+__device__ __forceinline__ void mul(float (&a)[VEC], const float (&b)[VEC]) {
+#pragma unroll
+  for (int e = 0; e + 1 < VEC; e += 2) {
+    const float2 v = __fmul2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+    a[e] = v.x, a[e + 1] = v.y;
+  }
+  if constexpr (VEC == 1) a[0] *= b[0];
 }
-template <class T, int VEC>
-__device__ __forceinline__ void store(void* base, size_t at, const float (&v)[VEC]) {
-  T* p = static_cast<T*>(base) + at;
-  if constexpr (VEC == 8) {
-    constexpr int kWords = sizeof(T) / 2;
-    uint4 w[kWords];
-    T* t = reinterpret_cast<T*>(w);
+template <int VEC>
+__device__ __forceinline__ void add(float (&a)[VEC], const float (&b)[VEC]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = from_f<T>(v[i]);
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
-  } else {
-    p[0] = from_f<T>(v[0]);
+  for (int e = 0; e + 1 < VEC; e += 2) {
+    const float2 v = __fadd2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+    a[e] = v.x, a[e + 1] = v.y;
   }
+  if constexpr (VEC == 1) a[0] += b[0];
+}
+template <int VEC>
+__device__ __forceinline__ void add_scaled(float (&a)[VEC], float s, const float (&b)[VEC]) {
+#pragma unroll
+  for (int e = 0; e + 1 < VEC; e += 2) {
+    const float2 v = __ffma2_rn(make_float2(s, s), make_float2(b[e], b[e + 1]), make_float2(a[e], a[e + 1]));
+    a[e] = v.x, a[e + 1] = v.y;
+  }
+  if constexpr (VEC == 1) a[0] = fmaf(s, b[0], a[0]);
 }
 
 // Sum over the WARPS warps of a row, the same in every thread. `turn` picks
@@ -106,11 +152,17 @@ __device__ __forceinline__ float row_sum(float v, float (*scratch)[WARPS], int& 
   return v;
 }
 
+// When a thread asks for the vectors (gate, weights, biases, scale, shift):
+// kAtOnce along with the row (a call of few rows: the time is one row's latency);
+// kBySum those of each norm before its sums; kByUse where they are used, which
+// leaves the registers for more rows at a time.
+enum When { kAtOnce, kBySum, kByUse };
+
 constexpr int kRowsPerBlock1 = 4;  // rows of a block where one warp takes a row
 
 // T: type of y, h and the vectors; X: type of x and x'. A row belongs to WARPS
 // warps, each thread holds NV groups of VEC values.
-template <class T, class X, int VEC, int NV, int WARPS>
+template <class T, class X, int VEC, int NV, int WARPS, When WHEN>
 __global__ void __launch_bounds__(WARPS == 1 ? kRowsPerBlock1 * 32 : WARPS * 32) residual_norm_kernel(const NormParams p) {
   __shared__ float scratch[2][WARPS];
   const int row = WARPS == 1 ? static_cast<int>(blockIdx.x) * kRowsPerBlock1 + static_cast<int>(warp_id()) : blockIdx.x;
@@ -120,18 +172,16 @@ __global__ void __launch_bounds__(WARPS == 1 ? kRowsPerBlock1 * 32 : WARPS * 32)
   const size_t base = static_cast<size_t>(row) * p.dim;
   const float inv_dim = 1.0f / static_cast<float>(p.dim);
   int turn = 0;
+  auto column = [&](int i) { return t * VEC + i * kStep; };
 
-  float v[NV][VEC], u[NV][VEC];
+  Raw<X, VEC> xr[NV];
+  Raw<T, VEC> yr[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = t * VEC + i * kStep;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[i][e] = u[i][e] = 0.f;
-    if (c < p.dim) {
-      load<X, VEC>(p.x, base + c, v[i]);
-      if (p.y) load<T, VEC>(p.y, base + c, u[i]);
+  for (int i = 0; i < NV; ++i)
+    if (column(i) < p.dim) {
+      xr[i].load_once(p.x, base + column(i));
+      if (p.y) yr[i].load_once(p.y, base + column(i));
     }
-  }
   // the row's sequence: the number of sequence ends at or before it; every
   // warp counts for itself
   int seq = 0;
@@ -139,129 +189,196 @@ __global__ void __launch_bounds__(WARPS == 1 ? kRowsPerBlock1 * 32 : WARPS * 32)
     if (row < p.offsets[0]) return;
     for (int b0 = 0; b0 < p.seqs; b0 += 32) {
       const int b = b0 + lane_id();
-      seq += __popc(__ballot_sync(0xffffffffu, b < p.seqs && p.offsets[b + 1 <= p.seqs ? b + 1 : p.seqs] <= row));
+      seq += __popc(__ballot_sync(0xffffffffu, b < p.seqs && p.offsets[min(b + 1, p.seqs)] <= row));
     }
     if (seq >= p.seqs) return;  // behind the last sequence: the row is left alone
   }
   const size_t mod = static_cast<size_t>(seq) * p.dim;
 
-  // 1 / deviation, after centring the values where the norm does
-  auto normalise = [&](float (&a)[NV][VEC], int kind) {
+  Raw<T, VEC> gate[NV], post_weight[NV], post_bias[NV], weight[NV], bias[NV], scale[NV], shift[NV];
+  auto ask = [&](Raw<T, VEC>(&v)[NV], const void* from, size_t at) {
+    if (from)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (column(i) < p.dim) v[i].load(from, at + column(i));
+  };
+  auto ask_post = [&] {
+    ask(post_weight, p.post_weight, 0);
+    ask(post_bias, p.post_bias, 0);
+    ask(gate, p.gate, mod);
+  };
+  auto ask_rest = [&] {
+    ask(weight, p.weight, 0);
+    ask(bias, p.bias, 0);
+    ask(scale, p.scale, mod);
+    ask(shift, p.shift, mod);
+  };
+  if constexpr (WHEN != kByUse) ask_post();
+  if constexpr (WHEN == kAtOnce) ask_rest();
+
+  float v[NV][VEC];
+  // group i of v times (1 + a vector) or plus a vector
+  auto times = [&](int i, Raw<T, VEC>(&w)[NV], const void* from, size_t at, float plus) {
+    if (!from) return;
+    if constexpr (WHEN == kByUse) w[i].load(from, at + column(i));
+    float f[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = plus + w[i].get(e);
+    mul(v[i], f);
+  };
+  auto plus = [&](int i, Raw<T, VEC>(&w)[NV], const void* from, size_t at) {
+    if (!from) return;
+    if constexpr (WHEN == kByUse) w[i].load(from, at + column(i));
+    float f[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = w[i].get(e);
+    add(v[i], f);
+  };
+  // centres the values where the norm does; returns 1 / deviation
+  auto deviation = [&](int kind) {
     if (kind == SVDQ_NORM_LAYER) {
+      float part[VEC] = {};
+#pragma unroll
+      for (int i = 0; i < NV; ++i) add(part, v[i]);
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s += a[i][e];
+      for (int e = 0; e < VEC; ++e) s += part[e];
       const float mean = row_sum<WARPS>(s, scratch, turn) * inv_dim;
+      float minus[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) minus[e] = -mean;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (t * VEC + i * kStep < p.dim)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) a[i][e] -= mean;
+        if (column(i) < p.dim) add(v[i], minus);
     }
+    float part[VEC] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) part[e] = fmaf(v[i][e], v[i][e], part[e]);
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int e = 0; e < VEC; ++e) s += part[e];
+    return 1.0f / sqrtf(row_sum<WARPS>(s, scratch, turn) * inv_dim + p.eps);
+  };
+  auto scaled = [&](int i, float r) {
+    float f[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s = fmaf(a[i][e], a[i][e], s);
-    const float r = 1.0f / sqrtf(row_sum<WARPS>(s, scratch, turn) * inv_dim + p.eps);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) a[i][e] *= r;
+    for (int e = 0; e < VEC; ++e) f[e] = r;
+    mul(v[i], f);
   };
 
   if (p.y) {
-    if (p.post_norm != SVDQ_NORM_NONE) normalise(u, p.post_norm);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[i][e] = column(i) < p.dim ? yr[i].get(e) : 0.f;
+    const float r = p.post_norm != SVDQ_NORM_NONE ? deviation(p.post_norm) : 1.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t * VEC + i * kStep;
+      const int c = column(i);
       if (c < p.dim) {
-        float w[VEC];
-        if (p.post_weight) {
-          load<T, VEC>(p.post_weight, c, w);
+        if (p.post_norm != SVDQ_NORM_NONE) scaled(i, r);
+        times(i, post_weight, p.post_weight, 0, 0.f);
+        plus(i, post_bias, p.post_bias, 0);
+        times(i, gate, p.gate, mod, 0.f);
+        float x[VEC];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) u[i][e] *= w[e];
-        }
-        if (p.post_bias) {
-          load<T, VEC>(p.post_bias, c, w);
+        for (int e = 0; e < VEC; ++e) x[e] = xr[i].get(e);
+        add_scaled(v[i], p.residual_scale, x);
+        Raw<X, VEC> out;
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) u[i][e] += w[e];
-        }
-        if (p.gate) {
-          load<T, VEC>(p.gate, mod + c, w);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) u[i][e] *= w[e];
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] = fmaf(p.residual_scale, v[i][e], u[i][e]);
-        store<X, VEC>(p.x_out, base + c, v[i]);
+        for (int e = 0; e < VEC; ++e) out.set(e, v[i][e]);
+        out.store(p.x_out, base + c);
       }
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[i][e] = column(i) < p.dim ? xr[i].get(e) : 0.f;
   }
   if (p.norm == SVDQ_NORM_NONE) return;
-  normalise(v, p.norm);
+  if constexpr (WHEN == kBySum) ask_rest();
+  const float r = deviation(p.norm);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = t * VEC + i * kStep;
+    const int c = column(i);
     if (c < p.dim) {
-      float w[VEC];
-      if (p.weight) {
-        load<T, VEC>(p.weight, c, w);
+      scaled(i, r);
+      times(i, weight, p.weight, 0, 0.f);
+      plus(i, bias, p.bias, 0);
+      times(i, scale, p.scale, mod, 1.f);
+      plus(i, shift, p.shift, mod);
+      Raw<T, VEC> out;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] *= w[e];
-      }
-      if (p.bias) {
-        load<T, VEC>(p.bias, c, w);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] += w[e];
-      }
-      if (p.scale) {
-        load<T, VEC>(p.scale, mod + c, w);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] *= 1.0f + w[e];
-      }
-      if (p.shift) {
-        load<T, VEC>(p.shift, mod + c, w);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] += w[e];
-      }
-      store<T, VEC>(p.h_out, base + c, v[i]);
+      for (int e = 0; e < VEC; ++e) out.set(e, v[i][e]);
+      out.store(p.h_out, base + c);
     }
   }
 }
 
-template <class T, class X, int VEC, int NV, int WARPS>
+template <class T, class X, int VEC, int NV, int WARPS, When WHEN>
 cudaError_t start(const NormParams& p, cudaStream_t st) {
-  if (WARPS == 1)
-    residual_norm_kernel<T, X, VEC, NV, WARPS><<<(p.rows + kRowsPerBlock1 - 1) / kRowsPerBlock1, kRowsPerBlock1 * 32, 0, st>>>(p);
-  else
-    residual_norm_kernel<T, X, VEC, NV, WARPS><<<p.rows, WARPS * 32, 0, st>>>(p);
+  const int blocks = WARPS == 1 ? (p.rows + kRowsPerBlock1 - 1) / kRowsPerBlock1 : p.rows;
+  residual_norm_kernel<T, X, VEC, NV, WARPS, WHEN><<<blocks, WARPS == 1 ? kRowsPerBlock1 * 32 : WARPS * 32, 0, st>>>(p);
   return cudaGetLastError();
 }
 
-// The fewest warps that hold the row at SHORT groups of VEC values a thread,
-// and LONG groups where even 16 warps need them (32 values of x and 32 of y a
-// thread: 512 threads still have the registers for that, 1024 would not).
-template <class T, class X, int VEC, int SHORT, int LONG>
-cudaError_t pick_warps(const NormParams& p, cudaStream_t st) {
-  const int groups = (p.dim + 32 * VEC - 1) / (32 * VEC);  // groups of VEC per lane of one warp
-  if (groups <= SHORT) return start<T, X, VEC, SHORT, 1>(p, st);
-  if (groups <= 4 * SHORT) return start<T, X, VEC, SHORT, 4>(p, st);
-  if (groups <= 8 * SHORT) return start<T, X, VEC, SHORT, 8>(p, st);
-  if (groups <= 16 * SHORT) return start<T, X, VEC, SHORT, 16>(p, st);
-  return start<T, X, VEC, LONG, 16>(p, st);
+// Rows of a multiple of 8 values (every row 16-byte aligned). Many rows: 2 to 4
+// groups a thread, and as few warps a row as that takes; few rows: as many warps
+// as the row has work for.
+template <class T, class X>
+cudaError_t pick_wide(const NormParams& p, bool many, cudaStream_t st) {
+  const int groups = (p.dim + 255) / 256;  // groups of 8 a lane, for one warp
+  if (many) {
+    if (groups <= 2) return start<T, X, 8, 2, 1, kBySum>(p, st);
+    if (groups <= 4) return start<T, X, 8, 2, 2, kBySum>(p, st);
+    if (groups <= 6) return start<T, X, 8, 3, 2, kBySum>(p, st);
+    if (groups <= 8) return start<T, X, 8, 2, 4, kBySum>(p, st);
+    if (groups <= 12) return start<T, X, 8, 3, 4, kBySum>(p, st);
+    if (groups <= 16) return start<T, X, 8, 2, 8, kByUse>(p, st);
+    if (groups <= 24) return start<T, X, 8, 3, 8, kBySum>(p, st);
+    if (groups <= 32) return start<T, X, 8, 4, 8, kByUse>(p, st);
+    return start<T, X, 8, 4, 16, kByUse>(p, st);
+  }
+  if (groups <= 1) return start<T, X, 8, 1, 1, kAtOnce>(p, st);
+  if (groups <= 4) return start<T, X, 8, 1, 4, kAtOnce>(p, st);
+  if (groups <= 8) return start<T, X, 8, 1, 8, kAtOnce>(p, st);
+  if (groups <= 16) return start<T, X, 8, 1, 16, kAtOnce>(p, st);
+  if (groups <= 32) return start<T, X, 8, 2, 16, kAtOnce>(p, st);
+  return start<T, X, 8, 4, 16, kByUse>(p, st);
+}
+
+// Other widths, by the same rule: pairs (an even dim) or single values.
+template <class T, class X, int VEC>
+cudaError_t pick_narrow(const NormParams& p, bool many, cudaStream_t st) {
+  const int groups = (p.dim + 32 * VEC - 1) / (32 * VEC);
+  constexpr When kWhen = VEC == 2 ? kBySum : kByUse;
+  if (many) {
+    if (groups <= 8) return start<T, X, VEC, 8, 1, kWhen>(p, st);
+    if (groups <= 32) return start<T, X, VEC, 8, 4, kWhen>(p, st);
+    if (groups <= 48) return start<T, X, VEC, 12, 4, kWhen>(p, st);
+    if (groups <= 96) return start<T, X, VEC, 12, 8, kWhen>(p, st);
+  } else {
+    if (groups <= 2) return start<T, X, VEC, 2, 1, kAtOnce>(p, st);
+    if (groups <= 8) return start<T, X, VEC, 2, 4, kAtOnce>(p, st);
+    if (groups <= 32) return start<T, X, VEC, 2, 16, kAtOnce>(p, st);
+    if (groups <= 64) return start<T, X, VEC, 4, 16, kAtOnce>(p, st);
+  }
+  return start<T, X, VEC, 32 / VEC, 16, kByUse>(p, st);
 }
 
 template <class T, class X>
-cudaError_t pick_vector(const NormParams& p, bool wide, cudaStream_t st) {
-  return wide ? pick_warps<T, X, 8, 2, 4>(p, st) : pick_warps<T, X, 1, 8, 32>(p, st);
+cudaError_t pick_vector(const NormParams& p, cudaStream_t st) {
+  const bool many = p.rows >= 200;  // at 3072: 600 rows 5.8 us so, 7.6 with the layout for few; 148 rows 3.1 with that
+  if (p.dim % 8 == 0) return pick_wide<T, X>(p, many, st);
+  return p.dim % 2 == 0 ? pick_narrow<T, X, 2>(p, many, st) : pick_narrow<T, X, 1>(p, many, st);
 }
 
 template <class T>
-cudaError_t pick_stream(const NormParams& p, bool x_float, bool wide, cudaStream_t st) {
-  return x_float ? pick_vector<T, float>(p, wide, st) : pick_vector<T, T>(p, wide, st);
+cudaError_t pick_stream(const NormParams& p, bool x_float, cudaStream_t st) {
+  return x_float ? pick_vector<T, float>(p, st) : pick_vector<T, T>(p, st);
 }
 
 constexpr int kMaxDim = 16384;  // 16 warps, 32 values a thread
@@ -299,11 +416,10 @@ extern "C" svdq_status svdq_residual_norm(const svdq_residual_norm_args* a, void
   if (reinterpret_cast<uintptr_t>(a->offsets) & 3) return fail(SVDQ_ERR_INVALID_ARG, "offsets must be 4-byte aligned");
   NormParams p{a->x, a->y, a->x_out, a->h_out, a->gate, a->post_weight, a->post_bias, a->weight, a->bias,
                a->scale, a->shift, a->offsets, a->rows, a->dim, a->seqs, a->residual_scale, a->eps, a->post_norm, a->norm};
-  // rows of a multiple of 8 values keep every row 16-byte aligned: wide loads
-  const bool wide = a->dim % 8 == 0, x_float = a->x_dtype == SVDQ_F32;
+  const bool x_float = a->x_dtype == SVDQ_F32;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->dtype == SVDQ_BF16 ? pick_stream<__nv_bfloat16>(p, x_float, wide, st)
-                                              : pick_stream<__half>(p, x_float, wide, st);
+  const cudaError_t e = a->dtype == SVDQ_BF16 ? pick_stream<__nv_bfloat16>(p, x_float, st)
+                                              : pick_stream<__half>(p, x_float, st);
   if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("residual norm: ") + cudaGetErrorString(e));
   return SVDQ_OK;
 }
