@@ -136,16 +136,18 @@ struct RowsSmem {
   static_assert(RB * kPitch * 4 <= kStages * kStage, "the partial sums reuse the stages");
 };
 
-__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t rank, float v) {
-  asm volatile(
-      "{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %0, %1;\n"
-      " st.shared::cluster.f32 [ra], %2;\n}\n" ::"r"(addr),
-      "r"(rank), "f"(v)
-      : "memory");
+// The shared::cluster address of `addr` in CTA `rank`.
+__device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 template <class T, int RB>
-__global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DenseParams p, const __grid_constant__ DenseMaps maps, int shares) {
+__global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DenseParams p, const __grid_constant__ DenseMaps maps, int share_bits) {
   using L = RowsSmem<RB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -155,10 +157,12 @@ __global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DensePar
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   constexpr uint32_t kCols = RB < 32 ? 32 : RB;
+  constexpr int kSliceBits = RB == 16 ? 3 : RB == 32 ? 4 : RB == 64 ? 5 : 6;  // log2 of RB / 2
 
   const int warp = warp_id(), lane = lane_id();
-  const int share = blockIdx.x % shares;  // also the rank in the cluster
-  const int n0 = blockIdx.x / shares * kRowsN;
+  const int shares = 1 << share_bits;
+  const int share = blockIdx.x & (shares - 1);  // also the rank in the cluster
+  const int n0 = (blockIdx.x >> share_bits) * kRowsN;
   const int m0 = blockIdx.y * RB;
   const int blocks = (p.K + kBK - 1) / kBK;
   const int first = static_cast<int>(static_cast<long long>(blocks) * share / shares);
@@ -227,18 +231,21 @@ __global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DensePar
   else __syncthreads();
 
   // partial sums to the owners of the rows: [share][row of the slice][column]
-  const int slice = RB / shares;
-  const uint32_t recv = smem_u32(smem);
+  const int slice = RB >> share_bits;
+  const uint32_t recv = smem_u32(smem) + (share * slice * L::kPitch + 32 * warp + lane) * 4;
 #pragma unroll
-  for (int c = 0; c < RB; c += 8) {
-    uint32_t r[8];
-    tmem_ld8(tmem + (static_cast<uint32_t>(32 * warp) << 16) + c, r);
+  for (int c = 0; c < RB; c += 16) {
+    if (m0 + c >= p.M) break;  // rows behind the last one are not read below
+    uint32_t r[16];
+    tmem_ld16(tmem + (static_cast<uint32_t>(32 * warp) << 16) + c, r);
     tmem_ld_wait();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int m = c + e, owner = m / slice;
-      const uint32_t at = recv + ((share * slice + m % slice) * L::kPitch + 32 * warp + lane) * 4;
-      if (m0 + m < p.M) store_cluster(at, owner, __uint_as_float(r[e]));
+    for (int e = 0; e < 16; e += 2) {  // a slice has two rows or more
+      const int owner = (c + e) / 2 >> (kSliceBits - share_bits);
+      const uint32_t at = recv + ((c + e) & (slice - 1)) * (L::kPitch * 4);
+      const uint32_t to = shares > 1 ? map_cluster(at, owner) : at;
+      store_cluster(to, __uint_as_float(r[e]));
+      store_cluster(to + L::kPitch * 4, __uint_as_float(r[e + 1]));
     }
   }
   tc_fence_before();
@@ -278,8 +285,9 @@ cudaError_t start_rows(const DenseParams& p, const DenseMaps& maps, int sms, cud
   const int tiles_n = (p.N + kRowsN - 1) / kRowsN, tiles_m = (p.M + RB - 1) / RB;
   // shares of K while they find free SMs and keep four blocks of K each
   const int room = (RB == 128 ? 1 : 2) * sms, blocks = (p.K + kBK - 1) / kBK;
-  int shares = 1;
-  while (shares < 8 && 2ll * shares * tiles_n * tiles_m <= room && blocks >= 8 * shares) shares *= 2;
+  int share_bits = 0;
+  while (share_bits < 3 && (2ll << share_bits) * tiles_n * tiles_m <= room && blocks >= 8 << share_bits) ++share_bits;
+  const int shares = 1 << share_bits;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tiles_n * shares, tiles_m);
   cfg.blockDim = dim3(kRowsThreads);
@@ -291,7 +299,7 @@ cudaError_t start_rows(const DenseParams& p, const DenseMaps& maps, int sms, cud
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dense_rows_kernel<T, RB>, p, maps, shares);
+  return cudaLaunchKernelEx(&cfg, dense_rows_kernel<T, RB>, p, maps, share_bits);
 }
 
 // ---------------------------------------------------------------- pair kernel
