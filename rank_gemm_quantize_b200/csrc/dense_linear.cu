@@ -69,22 +69,29 @@ __device__ __forceinline__ float2 gelu2(float2 t) {
   return make_float2(__fdividef(t.x, 1.f + exp2_fast(-g.x)), __fdividef(t.y, 1.f + exp2_fast(-g.y)));
 }
 
-__device__ __forceinline__ float2 activate(float2 t, int act) {
+__device__ __forceinline__ void activate(float2 (&v)[4], int act) {
   switch (act) {
     case SVDQ_ACT_RELU:
-      return make_float2(t.x < 0.f ? 0.f : t.x, t.y < 0.f ? 0.f : t.y);  // NaN stays
+#pragma unroll
+      for (float2& t : v) t = make_float2(t.x < 0.f ? 0.f : t.x, t.y < 0.f ? 0.f : t.y);  // NaN stays
+      break;
     case SVDQ_ACT_SILU:
-      return make_float2(__fdividef(t.x, 1.f + __expf(-t.x)), __fdividef(t.y, 1.f + __expf(-t.y)));
+#pragma unroll
+      for (float2& t : v) t = make_float2(__fdividef(t.x, 1.f + __expf(-t.x)), __fdividef(t.y, 1.f + __expf(-t.y)));
+      break;
     case SVDQ_ACT_GELU:
-      return gelu2(t);
-    case SVDQ_ACT_GELU_TANH: {
+#pragma unroll
+      for (float2& t : v) t = gelu2(t);
+      break;
+    case SVDQ_ACT_GELU_TANH:
       // (1 + tanh(z)) / 2 = 1 / (1 + exp(-2 z)); 2 log2(e) sqrt(2 / pi) = 2.302208198
-      const float2 t2 = __fmul2_rn(t, t);
-      const float2 z = __fmul2_rn(__ffma2_rn(t2, make_float2(0.10294324f, 0.10294324f), make_float2(2.3022082f, 2.3022082f)), t);
-      return make_float2(__fdividef(t.x, 1.f + exp2_fast(-z.x)), __fdividef(t.y, 1.f + exp2_fast(-z.y)));
-    }
-    default:
-      return t;
+#pragma unroll
+      for (float2& t : v) {
+        const float2 t2 = __fmul2_rn(t, t);
+        const float2 z = __fmul2_rn(__ffma2_rn(t2, make_float2(0.10294324f, 0.10294324f), make_float2(2.3022082f, 2.3022082f)), t);
+        t = make_float2(__fdividef(t.x, 1.f + exp2_fast(-z.x)), __fdividef(t.y, 1.f + exp2_fast(-z.y)));
+      }
+      break;
   }
 }
 
@@ -93,22 +100,18 @@ __device__ __forceinline__ float2 unpack(uint32_t w) {
   return make_float2(Half16<T>::to_float(w & 0xFFFFu), Half16<T>::to_float(w >> 16));
 }
 
-// Eight columns from n on of a row: bias, activation, residual (if p has one), one rounding.
+// Eight columns of a row: bias, activation, residual (what p has of them), one rounding.
 template <class T>
-__device__ __forceinline__ uint4 finish8(const DenseParams& p, int n, const float (&a)[8], const uint4& residual) {
+__device__ __forceinline__ uint4 finish8(const DenseParams& p, const uint4& bias, const float (&a)[8], const uint4& residual) {
   float2 v[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = make_float2(a[2 * e], a[2 * e + 1]);
   if (p.bias) {
-    const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + n));
-    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+    const uint32_t w[4] = {bias.x, bias.y, bias.z, bias.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(v[e], unpack<T>(w[e]));
   }
-  if (p.act != SVDQ_ACT_NONE) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = activate(v[e], p.act);
-  }
+  activate(v, p.act);
   if (p.residual) {
     const uint32_t w[4] = {residual.x, residual.y, residual.z, residual.w};
 #pragma unroll
@@ -122,18 +125,20 @@ constexpr int kBK = 64;
 
 // ---------------------------------------------------------------- rows kernel
 constexpr int kRowsN = 128;  // columns of W of a CTA
-constexpr int kRowsThreads = 128;
+constexpr int kRowsThreads = 256, kRowsWarps = 8;
 
 template <int RB>
 struct RowsSmem {
   static constexpr int kW = kRowsN * kBK * 2;  // 16 KB
   static constexpr int kX = RB * kBK * 2;
   static constexpr int kStage = kW + kX;
-  static constexpr int kStages = RB == 128 ? 6 : 96 * 1024 / kStage;  // up to 64 rows: two CTAs an SM
   static constexpr int kPitch = kRowsN + 4;  // floats of a row of partial sums
-  static constexpr int kBars = kStages * kStage;
+  static constexpr int kSums = RB * kPitch * 4;
+  static constexpr int kRoom = (RB == 128 ? 200 : 110) * 1024;  // up to 64 rows: two CTAs an SM
+  static constexpr int kStages = (kRoom - kSums) / kStage;
+  static constexpr int kSumsOff = kStages * kStage;
+  static constexpr int kBars = kSumsOff + kSums;
   static constexpr int kTotal = kBars + 256 + 1024;
-  static_assert(RB * kPitch * 4 <= kStages * kStage, "the partial sums reuse the stages");
 };
 
 // The shared::cluster address of `addr` in CTA `rank`.
@@ -145,6 +150,11 @@ __device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void store_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <class T, int RB>
 __global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DenseParams p, const __grid_constant__ DenseMaps maps, int share_bits) {
@@ -154,10 +164,10 @@ __global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DensePar
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* empty = full + L::kStages;
   uint64_t* acc_full = empty + L::kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  uint64_t* sums_full = acc_full + 1;  // the shares' sums of this CTA's rows have arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   constexpr uint32_t kCols = RB < 32 ? 32 : RB;
-  constexpr int kSliceBits = RB == 16 ? 3 : RB == 32 ? 4 : RB == 64 ? 5 : 6;  // log2 of RB / 2
 
   const int warp = warp_id(), lane = lane_id();
   const int shares = 1 << share_bits;
@@ -168,14 +178,31 @@ __global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DensePar
   const int first = static_cast<int>(static_cast<long long>(blocks) * share / shares);
   const int last = static_cast<int>(static_cast<long long>(blocks) * (share + 1) / shares);
 
+  constexpr int kRowBits = RB == 16 ? 4 : RB == 32 ? 5 : RB == 64 ? 6 : 7;
+  const int slice_bits = kRowBits - share_bits, slice = 1 << slice_bits;  // rows that each CTA of the cluster finishes
+  const int mine = max(0, min(slice, p.M - m0 - share * slice));
+
+  // The first loads need no one but the barriers: they start before tensor
+  // memory is there.
+  const int ahead = min(last - first, L::kStages);
+  auto load = [&](int n) {
+    const int s = n % L::kStages;
+    uint8_t* st = smem + s * L::kStage;
+    mbar_arrive_expect_tx(&full[s], L::kStage);
+    tma_load_2d(st, &maps.w, &full[s], n0, (first + n) * kBK);
+    tma_load_2d(st + 8192, &maps.w, &full[s], n0 + 64, (first + n) * kBK);
+    tma_load_2d(st + L::kW, &maps.x, &full[s], (first + n) * kBK, m0);
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(acc_full, 1);
+    mbar_init(sums_full, shares * kRowsWarps);
     *abort_flag = 0;
     fence_barrier_init();
+    for (int n = 0; n < ahead; ++n) load(n);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, kCols);
@@ -183,25 +210,22 @@ __global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DensePar
   }
   tc_fence_before();
   __syncthreads();
+  if (shares > 1) cluster_arrive();  // this CTA's barriers are ready for the others
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
     if (lane == 0) {
-      int i = first;
-      for (; i < last; ++i) {
-        const int n = i - first, s = n % L::kStages;
-        if (!mbar_wait(&empty[s], ((n / L::kStages) & 1) ^ 1, abort_flag, &g_status)) break;
-        uint8_t* st = smem + s * L::kStage;
-        mbar_arrive_expect_tx(&full[s], L::kStage);
-        tma_load_2d(st, &maps.w, &full[s], n0, i * kBK);
-        tma_load_2d(st + 8192, &maps.w, &full[s], n0 + 64, i * kBK);
-        tma_load_2d(st + L::kW, &maps.x, &full[s], i * kBK, m0);
-      }
-      if (i < last) {  // gave up: the copies in flight land before shared memory is used again
+      int n = ahead;
+      for (; n < last - first; ++n)
+        if (mbar_wait(&empty[n % L::kStages], ((n / L::kStages) & 1) ^ 1, abort_flag, &g_status))
+          load(n);
+        else
+          break;
+      if (n < last - first) {  // gave up: the copies in flight land before the CTA ends
         volatile int no_abort = 0;
-        for (int n = std::max(0, i - first - L::kStages); n < i - first; ++n)
-          mbar_wait(&full[n % L::kStages], (n / L::kStages) & 1, &no_abort, nullptr);
+        for (int e = std::max(0, n - L::kStages); e < n; ++e)
+          mbar_wait(&full[e % L::kStages], (e / L::kStages) & 1, &no_abort, nullptr);
       }
     }
     __syncwarp();
@@ -224,53 +248,63 @@ __global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DensePar
     }
     __syncwarp();
   }
+  // Thread t finishes columns 8 (t % 16) .. of rows t / 16, t / 16 + 16, .. of the
+  // slice; the bias and the first row's residual are asked for ahead. The
+  // loops below are kept rolled: their code runs once, and fetching it costs.
+  const int c8 = threadIdx.x % (kRowsN / 8) * 8, r0 = threadIdx.x / (kRowsN / 8), n8 = n0 + c8;
+  uint4 bias = make_uint4(0, 0, 0, 0);
+  if (p.bias && n8 < p.N) bias = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + n8));
+  auto at = [&](int r) { return static_cast<size_t>(m0 + share * slice + r) * p.N + n8; };
+  auto residual = [&](int r) {
+    if (!p.residual || r >= mine || n8 >= p.N) return make_uint4(0, 0, 0, 0);
+    return *reinterpret_cast<const uint4*>(static_cast<const T*>(p.residual) + at(r));
+  };
+  uint4 res = residual(r0);
   volatile int no_abort = 0;
   mbar_wait(acc_full, 0, &no_abort, &g_status);
   tc_fence_after();
-  if (shares > 1) cluster_sync_all();  // every CTA of the cluster is done with its stages
-  else __syncthreads();
 
-  // partial sums to the owners of the rows: [share][row of the slice][column]
-  const int slice = RB >> share_bits;
-  const uint32_t recv = smem_u32(smem) + (share * slice * L::kPitch + 32 * warp + lane) * 4;
-#pragma unroll
-  for (int c = 0; c < RB; c += 16) {
+  // The partial sums go to the owners of the rows, [share][row of the slice][column];
+  // two warps a quarter of the lanes, each with every other 16 rows.
+  if (shares > 1) cluster_wait();
+  const uint32_t column = 32 * (warp & 3) + lane;
+  const uint32_t here = smem_u32(smem + L::kSumsOff) + (share * slice * L::kPitch + column) * 4;
+#pragma unroll 1
+  for (int c = 16 * (warp >> 2); c < RB; c += 32) {
     if (m0 + c >= p.M) break;  // rows behind the last one are not read below
     uint32_t r[16];
-    tmem_ld16(tmem + (static_cast<uint32_t>(32 * warp) << 16) + c, r);
+    tmem_ld16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, r);
     tmem_ld_wait();
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {  // a slice has two rows or more
-      const int owner = (c + e) / 2 >> (kSliceBits - share_bits);
-      const uint32_t at = recv + ((c + e) & (slice - 1)) * (L::kPitch * 4);
-      const uint32_t to = shares > 1 ? map_cluster(at, owner) : at;
+      const uint32_t to = map_cluster(here + ((c + e) & (slice - 1)) * (L::kPitch * 4), (c + e) >> slice_bits);
       store_cluster(to, __uint_as_float(r[e]));
       store_cluster(to + L::kPitch * 4, __uint_as_float(r[e + 1]));
     }
   }
   tc_fence_before();
-  if (shares > 1) cluster_sync_all();
-  else __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kCols);
-  }
-  const float* sums = reinterpret_cast<const float*>(smem);
-  for (int i = threadIdx.x; i < slice * (kRowsN / 8); i += kRowsThreads) {
-    const int r = i / (kRowsN / 8), c = i % (kRowsN / 8) * 8;
-    const int m = m0 + share * slice + r, n = n0 + c;
-    if (m >= p.M || n >= p.N) continue;
+  __syncwarp();
+  if (lane < shares) arrive_cluster(map_cluster(smem_u32(sums_full), lane));
+  mbar_wait_cluster(sums_full, 0, &no_abort, &g_status);
+  const uint8_t* sums = smem + L::kSumsOff;
+#pragma unroll 1
+  for (int r = r0; r < mine; r += kRowsThreads / (kRowsN / 8)) {
+    const uint4 now = res;
+    res = residual(r + kRowsThreads / (kRowsN / 8));
+    if (n8 >= p.N) continue;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < shares; ++s) {
-      const float4* src = reinterpret_cast<const float4*>(sums + (s * slice + r) * L::kPitch + c);
+      const float4* src = reinterpret_cast<const float4*>(sums + ((s * slice + r) * L::kPitch + c8) * 4);
       const float4 a = src[0], b = src[1];
       v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
       v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
-    const size_t at = static_cast<size_t>(m) * p.N + n;
-    uint4 res = make_uint4(0, 0, 0, 0);
-    if (p.residual) res = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.residual) + at);
-    *reinterpret_cast<uint4*>(static_cast<T*>(p.Y) + at) = finish8<T>(p, n, v, res);
+    *reinterpret_cast<uint4*>(static_cast<T*>(p.Y) + at(r)) = finish8<T>(p, bias, v, now);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
   }
 }
 
@@ -471,7 +505,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           float x[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(a[8 * v + e]);
-          const uint4 y = n < p.N ? finish8<T>(p, n, x, r[v]) : make_uint4(0, 0, 0, 0);
+          uint4 bias = make_uint4(0, 0, 0, 0);
+          if (p.bias && n < p.N) bias = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + n));
+          const uint4 y = finish8<T>(p, bias, x, r[v]);
           *reinterpret_cast<uint4*>(out + ((v ^ ((lane >> 1) & 3)) << 4)) = y;
         }
         fence_proxy_async_smem();
