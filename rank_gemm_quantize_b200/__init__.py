@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 from enum import IntEnum
 from typing import Optional
@@ -82,6 +83,14 @@ class _ResidualNorm(ctypes.Structure):
                                            "bias", "scale", "shift", "offsets")]
 
 
+def _packer(cls):
+    """Packs a call's arguments as the C struct, without the cost of a ctypes object (0 for NULL)."""
+    code = {ctypes.c_int: "i", ctypes.c_float: "f", ctypes.c_void_p: "P", ctypes.c_longlong: "q"}
+    return struct.Struct("@" + "".join(code[t] for _, t in cls._fields_)).pack
+
+
+_pack_attention, _pack_residual_norm = _packer(_Attention), _packer(_ResidualNorm)
+
 # Every symbol include/svdq.h declares, with its ctypes signature.
 _VP, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 SIGNATURES = {
@@ -111,10 +120,10 @@ SIGNATURES = {
     "svdq_w4a16_forward": [_VP, _VP, _I, _VP, _VP],
     "svdq_w4a16_export": [_VP, _VP, _VP, _VP],
     "svdq_w4a16_destroy": [_VP],
-    "svdq_attention_workspace_size": [ctypes.POINTER(_Attention), ctypes.POINTER(_SZ)],
-    "svdq_attention_forward": [ctypes.POINTER(_Attention), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP],
+    "svdq_attention_workspace_size": [_VP, ctypes.POINTER(_SZ)],
+    "svdq_attention_forward": [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP],
     "svdq_dense_linear_forward": [_I, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP],
-    "svdq_residual_norm": [ctypes.POINTER(_ResidualNorm), _VP],
+    "svdq_residual_norm": [_VP, _VP],
     "svdq_operator_status": [_VP],
 }
 
@@ -514,7 +523,8 @@ def _call_stream(device: int, stream, *made: torch.Tensor) -> int:
     return handle
 
 
-def _attention_config(q, k, v, batch, causal, scale) -> _Attention:
+def _attention_shapes(q, k, v, batch):
+    """(dtype, batch, q rows, k rows, q heads, kv heads, dim) of the calls' config, checked."""
     shape, keys = q.shape, k.shape
     if len(shape) != 3 or len(keys) != 3 or keys != v.shape or shape[2] != keys[2]:
         raise ValueError(f"q must be [rows, heads, dim], k and v [rows, heads, dim] alike, got {tuple(shape)}, "
@@ -524,21 +534,16 @@ def _attention_config(q, k, v, batch, causal, scale) -> _Attention:
         raise ValueError("q, k and v must all be bfloat16 or all float16")
     if k.get_device() != device or v.get_device() != device:
         raise ValueError("q, k and v must be on one device")
-    (qr, qh, q1), (kr, kh, k1), (vr, vh, v1) = q.stride(), k.stride(), v.stride()
-    if q1 != 1 or k1 != 1 or v1 != 1:
-        raise ValueError("the values of a head of q, k and v must be contiguous")
-    rows, heads, dim = shape
-    return _Attention(_DTYPE[dtype], batch, rows, keys[0], heads, keys[1], dim, 1 if causal else 0,
-                      dim ** -0.5 if scale is None else scale, qr, qh, kr, kh, vr, vh)
+    return _DTYPE[dtype], batch, shape[0], keys[0], shape[1], keys[1], shape[2]
 
 
 @functools.lru_cache(maxsize=4096)
-def _attention_need(device: int, *shape: int) -> int:
+def _attention_need(device: int, *shapes: int) -> int:
     """svdq_attention_workspace_size, which goes by the device and the shapes alone."""
-    dtype, batch, q_rows, k_rows, q_heads, kv_heads, dim = shape
+    heads, kv_heads, dim = shapes[4:]
     n = ctypes.c_size_t()
     _check(lib().svdq_attention_workspace_size(
-        ctypes.byref(_Attention(*shape, 0, 1.0, q_heads * dim, dim, kv_heads * dim, dim, kv_heads * dim, dim)), ctypes.byref(n)))
+        _pack_attention(*shapes, 0, 1.0, heads * dim, dim, kv_heads * dim, dim, kv_heads * dim, dim), ctypes.byref(n)))
     return n.value
 
 
@@ -546,8 +551,7 @@ def attention_workspace_size(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     """Bytes of workspace attention() needs for these shapes."""
     device = _place(q)
     with torch.cuda.device(device):
-        c = _attention_config(q, k, v, batch, False, None)
-        return _attention_need(device, c.dtype, batch, c.q_rows, c.k_rows, c.q_heads, c.kv_heads, c.head_dim)
+        return _attention_need(device, *_attention_shapes(q, k, v, batch))
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Optional[torch.Tensor] = None,
@@ -582,8 +586,12 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opti
             ko = _offsets("k_offsets", k_offsets, device)
             if k_offsets.shape[0] != batch + 1:
                 raise ValueError("q_offsets and k_offsets must be of the same length")
-    cfg = _attention_config(q, k, v, batch, causal, scale)
-    need = _attention_need(device, cfg.dtype, batch, cfg.q_rows, cfg.k_rows, cfg.q_heads, cfg.kv_heads, cfg.head_dim)
+    shapes = _attention_shapes(q, k, v, batch)
+    (qr, qh, q1), (kr, kh, k1), (vr, vh, v1) = q.stride(), k.stride(), v.stride()
+    if q1 != 1 or k1 != 1 or v1 != 1:
+        raise ValueError("the values of a head of q, k and v must be contiguous")
+    cfg = _pack_attention(*shapes, 1 if causal else 0, shapes[6] ** -0.5 if scale is None else scale, qr, qh, kr, kh, vr, vh)
+    need = _attention_need(device, *shapes)
     made_out = made_workspace = None
     if out is None:
         out = made_out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(tuple(q.shape))
@@ -594,7 +602,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opti
     elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != device:
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    _check(lib().svdq_attention_forward(ctypes.byref(cfg), q.data_ptr(), k.data_ptr(), v.data_ptr(), qo, ko, o, ws, size,
+    _check(lib().svdq_attention_forward(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), qo, ko, o, ws, size,
                                         _call_stream(device, stream, made_out, made_workspace)))
     return out
 
@@ -665,34 +673,36 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
                                  scale=scale, shift=shift, eps=eps, dtype=dtype, out_x=out_x, out_h=out_h, stream=stream)
     shape = x.shape
     rows, dim = shape
-    seqs, off, made_x, made_h = 1, None, None, None
+    x_kind = x.dtype
+    seqs, off, made_x, made_h, x_out, h_out = 1, None, None, None, 0, 0
     if offsets is not None:
         off, seqs = _offsets("offsets", offsets, device), offsets.shape[0] - 1
-
-    def vector(name, t):
-        return None if t is None else _operand(name, t, kind, device, (dim,))
-
-    def row_of_sequence(name, t):
-        return None if t is None else _operand(name, t, kind, device, (dim,) if seqs == 1 and t.dim() == 1 else (seqs, dim))
-
+    of_row, of_seq = (dim,), (seqs, dim)
+    if seqs == 1:  # one row for all may come without its first dimension
+        gate, scale, shift = (None if t is None else t.view(1, -1) if t.dim() == 1 else t for t in (gate, scale, shift))
     if y is not None:
         if out_x is None:
             out_x = made_x = torch.empty_like(x, memory_format=torch.contiguous_format)
+        x_out = _operand("out_x", out_x, x_kind, device, shape)
     elif out_x is not None:
         raise ValueError("without y there is no out_x")
     if norm is not None:
         if out_h is None:
             out_h = made_h = torch.empty_like(x if y is None else y, dtype=kind, memory_format=torch.contiguous_format)
+        h_out = _operand("out_h", out_h, kind, device, shape)
     elif out_h is not None:
         raise ValueError("without a norm there is no out_h")
-    args = _ResidualNorm(
-        _DTYPE[kind], _DTYPE[x.dtype], rows, dim, seqs, _NORM[post_norm], _NORM[norm], residual_scale, eps,
-        _operand("x", x, x.dtype, device, shape), None if y is None else _operand("y", y, kind, device, shape),
-        None if y is None else _operand("out_x", out_x, x.dtype, device, shape),
-        None if norm is None else _operand("out_h", out_h, kind, device, shape),
-        row_of_sequence("gate", gate), vector("post_weight", post_weight), vector("post_bias", post_bias),
-        vector("weight", weight), vector("bias", bias), row_of_sequence("scale", scale), row_of_sequence("shift", shift), off)
-    _check(lib().svdq_residual_norm(ctypes.byref(args), _call_stream(device, stream, made_x, made_h)))
+    args = _pack_residual_norm(
+        _DTYPE[kind], _DTYPE[x_kind], rows, dim, seqs, _NORM[post_norm], _NORM[norm], residual_scale, eps,
+        _operand("x", x, x_kind, device, shape), 0 if y is None else _operand("y", y, kind, device, shape), x_out, h_out,
+        0 if gate is None else _operand("gate", gate, kind, device, of_seq),
+        0 if post_weight is None else _operand("post_weight", post_weight, kind, device, of_row),
+        0 if post_bias is None else _operand("post_bias", post_bias, kind, device, of_row),
+        0 if weight is None else _operand("weight", weight, kind, device, of_row),
+        0 if bias is None else _operand("bias", bias, kind, device, of_row),
+        0 if scale is None else _operand("scale", scale, kind, device, of_seq),
+        0 if shift is None else _operand("shift", shift, kind, device, of_seq), off or 0)
+    _check(lib().svdq_residual_norm(args, _call_stream(device, stream, made_x, made_h)))
     return x if y is None else out_x, out_h
 
 

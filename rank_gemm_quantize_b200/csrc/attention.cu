@@ -48,7 +48,8 @@ svdq_status check(const svdq_attention_config* c) {
 
 struct Plan {
   int sms, chunk, max_slots;
-  bool prompt;  // attention_prompt.cu, or attention_step.cu
+  bool prompt;   // attention_prompt.cu, or attention_step.cu
+  bool cluster;  // attention_step.cu: an item's shares are a cluster
   size_t ml, total;
 };
 
@@ -71,6 +72,12 @@ svdq_status plan(const svdq_attention_config* c, Plan* out) {
     tiles = rows / kPromptRows + c->batch;
     const long long shares = p.sms / (tiles * c->kv_heads);
     keys = shares > 1 ? std::max<long long>(512, c->k_rows / shares) : c->k_rows;
+  } else if ((rows / kStepRows + c->batch) * c->kv_heads * kStepCluster <= 2 * p.sms &&
+             c->k_rows <= static_cast<long long>(1024) * kStepCluster * c->batch) {
+    // all clusters run at once, and their shares of the keys are short
+    p.cluster = true;
+    tiles = 0;
+    keys = c->k_rows;
   } else {
     // two CTAs an SM, four shares a CTA
     tiles = std::min<long long>(kStepSplitTiles, (rows + kStepRows - 1) / kStepRows);
@@ -158,7 +165,7 @@ svdq_status svdq_attention_forward(const svdq_attention_config* cfg, const void*
     return fail(SVDQ_ERR_CUDA, "cuTensorMapEncodeTiled (keys or values) failed");
   const bool bf16 = cfg->dtype == SVDQ_BF16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = pl.prompt ? launch_attention_prompt(p, maps, bf16, st) : launch_attention_step(p, maps, bf16, pl.sms, st);
+  cudaError_t e = pl.prompt ? launch_attention_prompt(p, maps, bf16, st) : launch_attention_step(p, maps, bf16, pl.cluster, pl.sms, st);
   if (e == cudaSuccess && pl.max_slots > 0) e = launch_attention_join(p, bf16, st);
   if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("attention kernel: ") + cudaGetErrorString(e));
   return SVDQ_OK;

@@ -169,6 +169,7 @@ __device__ bool find_item(const AttnParams& p, Search& at, int idx, Found* found
 constexpr int kStepRows = 16;
 constexpr int kStepKeys = 64;
 constexpr int kStepSplitTiles = 4;
+constexpr int kStepCluster = 8;  // CTAs of an item that join within a cluster
 // Many queries (attention_prompt.cu): rows of a CTA (two tensor-memory tiles), key tile.
 constexpr int kPromptRows = 256;
 constexpr int kPromptKeys = 128;
@@ -178,6 +179,6 @@ cudaError_t launch_attention_prompt(const AttnParams& p, const AttnMaps& maps, b
 // Joins the shares of the sequences that have several (after either kernel).
 cudaError_t launch_attention_join(const AttnParams& p, bool bf16, cudaStream_t st);
 cudaError_t take_status_attention_step(int* status, cudaStream_t st);
-cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, int sms, cudaStream_t st);
+cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, bool cluster, int sms, cudaStream_t st);
 
 }  // namespace svdq

@@ -9,7 +9,10 @@
 // takes 16 of them: scores by mma.m16n8k16, softmax statistics and the product
 // with V in registers, with no exchange between warps until the item's end. The
 // shares' results (unnormalised float sums, maximum, sum) go to the workspace,
-// or straight to the output where a sequence has one share.
+// or straight to the output where a sequence has one share. A call of so few and
+// short sequences that eight CTAs an item are all there is to gain takes one
+// launch: the eight are a cluster, cut the keys evenly and join their results
+// through distributed shared memory.
 //
 // Memory bounds it: 4 dim bytes a key and key head; 16 rows cost a fraction of
 // the tensor pipe, which is why the narrow mma is used here and a 128-row
@@ -32,8 +35,11 @@ struct StepSmem {
   static constexpr int kStage = 2 * kTile;
   static constexpr int kStages = 96 * 1024 / kStage;  // 96 KB of loads: two CTAs an SM
   static constexpr int kPitch = DP + 4;               // floats of a row when the warps' sums are joined
-  static constexpr int kBars = kStages * kStage;
-  static constexpr int kTotal = kBars + 1024 + 1024;
+  // results of the cluster's CTAs for the two rows that this one finishes
+  static constexpr int kOwnRows = kStepRows / kStepCluster;
+  static constexpr int kSums = kStages * kStage;
+  static constexpr int kBars = kSums + kStepCluster * kOwnRows * kPitch * 4;
+  static constexpr int kTotal = kBars + 256 + 1024;
   static_assert(kWarps * kStepRows * kPitch * 4 <= kStages * kStage, "the join reuses the stages");
 };
 
@@ -67,7 +73,13 @@ __device__ __forceinline__ uint32_t tile_at(int key, int piece) {
   return (piece >> 3) * (kStepKeys * 128) + key * 128 + (((piece & 7) ^ (key & 7)) << 4);
 }
 
-template <class T, int DP>
+__device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+template <class T, int DP, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps) {
   using L = StepSmem<DP>;
   extern __shared__ uint8_t smem_raw[];
@@ -79,6 +91,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
   __shared__ int spoiled;
   __shared__ int abort_word;
   __shared__ float warp_ml[kWarps][kStepRows][2];
+  __shared__ float2 share_ml[kStepCluster][L::kOwnRows];
   volatile int* abort_flag = &abort_word;
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
@@ -93,12 +106,16 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
     fence_barrier_init();
   }
   __syncthreads();
+  if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
   uint32_t used = 0;    // key tiles since the kernel's start
   uint32_t issued = 0;  // ... and how many of them thread 0 has asked for
   Search at{0, 0, 0};
-  for (int item = blockIdx.x;; item += gridDim.x) {
-    if (!find_item<kWarps>(p, at, item, &found, sums)) return;
+  for (int item = CLUSTER ? blockIdx.x / kStepCluster : blockIdx.x;; item += gridDim.x) {
+    if (!find_item<kWarps>(p, at, item, &found, sums)) {  // a cluster's CTAs alike
+      if (CLUSTER) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      return;
+    }
     const Found f = found;
     int qs, ql, ks, kl;
     seq_extent(p.q_offsets, f.b, p.q_rows, qs, ql);
@@ -106,12 +123,20 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
     const int rows = ql * p.group;
     const int row0 = f.tile * kStepRows;
     // keys [k_begin, k_end) of this share; row r sees keys <= limit(r)
-    const int k_begin = f.chunks > 1 ? f.chunk * p.chunk : 0;
     auto limit = [&](int row) {
       if (row >= rows) return -1;
       return p.causal ? min(row / p.group + kl - ql, kl - 1) : kl - 1;
     };
-    const int k_end = min(f.chunks > 1 ? k_begin + p.chunk : kl, limit(min(row0 + kStepRows, rows) - 1) + 1);
+    const int seen = limit(min(row0 + kStepRows, rows) - 1) + 1;  // keys that some row sees
+    int k_begin, k_end;
+    if (CLUSTER) {
+      const int all = (max(seen, 0) + kStepKeys - 1) / kStepKeys, share = blockIdx.x % kStepCluster;
+      k_begin = all * share / kStepCluster * kStepKeys;
+      k_end = min(all * (share + 1) / kStepCluster * kStepKeys, seen);
+    } else {
+      k_begin = f.chunks > 1 ? f.chunk * p.chunk : 0;
+      k_end = min(f.chunks > 1 ? k_begin + p.chunk : kl, seen);
+    }
     const int first_limit = limit(row0);
     const int tiles = k_end > k_begin ? (k_end - k_begin + kStepKeys - 1) / kStepKeys : 0;
 
@@ -267,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
         for (uint32_t n = issued > L::kStages ? issued - L::kStages : 0; n < issued; ++n)
           mbar_wait(&full[n % L::kStages], (n / L::kStages) & 1, &no_abort, nullptr);
       }
-      return;
+      if (!CLUSTER) return;  // a cluster's CTAs meet below, whatever their results are worth
+      __syncthreads();
     }
     used += tiles;
     // join the warps: each row's maximum, sum and products
@@ -287,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
             make_float2(o[n][2 * h], o[n][2 * h + 1]);
     __syncthreads();
     const int r = tid >> 3, row = row0 + r;
+    if (CLUSTER) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
     if (row < rows) {
       float top = -INFINITY, total = 0.f, w[kWarps];
 #pragma unroll
@@ -297,12 +324,14 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
         w[a] = exp2_fast(fmaf(warp_ml[a][r][0], p.scale_log2, -base));
         total = fmaf(warp_ml[a][r][1], w[a], total);
       }
-      const bool split = f.chunks > 1;
+      const bool split = CLUSTER || f.chunks > 1;
       const float norm = split || total == 0.f ? 1.f : 1.f / total;
       const int row_limit = limit(row);
       const int share = f.slots + f.tile * f.chunks + f.chunk;
       const size_t slot = (static_cast<size_t>(share) * p.kv_heads + hk) * kStepRows + r;
       const bool fits = share < p.max_slots;
+      const int owner = r / L::kOwnRows, slot_row = blockIdx.x % kStepCluster * L::kOwnRows + r % L::kOwnRows;
+      const uint32_t to = CLUSTER ? map_cluster(smem_u32(smem + L::kSums) + slot_row * (L::kPitch * 4), owner) : 0;
 #pragma unroll
       for (int c0 = 0; c0 < DP; c0 += 32) {
         const int c = c0 + (tid & 7) * 4;
@@ -326,7 +355,10 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
               if ((e[j] & Half16<T>::kExp) == Half16<T>::kExp) x[j] += Half16<T>::to_float(e[j]);
           }
         }
-        if (split) {
+        if (CLUSTER) {
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + c * 4), "f"(acc.x), "f"(acc.y), "f"(acc.z), "f"(acc.w)
+                       : "memory");
+        } else if (split) {
           if (fits) *reinterpret_cast<float4*>(p.part + slot * DP + c) = acc;
         } else if (c < p.dim) {
           uint2 v;
@@ -336,7 +368,41 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
                                     (static_cast<size_t>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim + c) = v;
         }
       }
-      if (split && fits && (tid & 7) == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, total);
+      if (CLUSTER) {
+        if ((tid & 7) == 0)
+          asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(map_cluster(smem_u32(&share_ml[0][0]) + slot_row * 8, owner)),
+                       "f"(top), "f"(total)
+                       : "memory");
+      } else if (split && fits && (tid & 7) == 0) {
+        *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, total);
+      }
+    }
+    if (CLUSTER) {
+      cluster_sync_all();  // the rows of this CTA have arrived from all eight
+      constexpr int kThreadsRow = kThreads / L::kOwnRows, kCols = DP / kThreadsRow;
+      const int own = tid / kThreadsRow, c = tid % kThreadsRow * kCols, mine = row0 + blockIdx.x % kStepCluster * L::kOwnRows + own;
+      if (mine < rows && c < p.dim) {
+        float top = -INFINITY, total = 0.f, o[kCols] = {};
+#pragma unroll
+        for (int s = 0; s < kStepCluster; ++s) top = fmaxf(top, share_ml[s][own].x);
+        const float base = (top == -INFINITY ? 0.f : top) * p.scale_log2;
+#pragma unroll
+        for (int s = 0; s < kStepCluster; ++s) {
+          const float2 ml = share_ml[s][own];
+          const float w = exp2_fast(fmaf(ml.x, p.scale_log2, -base));
+          total = fmaf(ml.y, w, total);
+#pragma unroll
+          for (int e = 0; e < kCols; ++e)
+            o[e] = fmaf(reinterpret_cast<const float*>(smem + L::kSums)[(s * L::kOwnRows + own) * L::kPitch + c + e], w, o[e]);
+        }
+        const float norm = total == 0.f ? 1.f : 1.f / total;
+        T* out = static_cast<T*>(p.out) + (static_cast<size_t>(qs + mine / p.group) * p.q_heads + hk * p.group + mine % p.group) * p.dim + c;
+        if constexpr (kCols == 2)
+          *reinterpret_cast<uint32_t*>(out) = Half16<T>::pack(o[0] * norm, o[1] * norm);
+        else
+          *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(Half16<T>::pack(o[0] * norm, 0.f));
+      }
+      return;
     }
     fence_proxy_async_smem();  // the stages are loaded again by TMA
     __syncthreads();
@@ -414,20 +480,32 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnPara
   }
 }
 
-template <class T, int DP>
+template <class T, int DP, bool CLUSTER>
 cudaError_t start(const AttnParams& p, const AttnMaps& maps, int sms, cudaStream_t st) {
   using L = StepSmem<DP>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(attention_step_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+    return cudaFuncSetAttribute(attention_step_kernel<T, DP, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
   });
   if (e != cudaSuccess) return e;
-  // two CTAs an SM go through the items; no more of them than items
-  const long long rows = static_cast<long long>(p.q_rows) * p.group;
-  const long long items = p.max_slots + rows / kStepRows + p.batch;
-  const long long fill = (2ll * sms + p.kv_heads - 1) / p.kv_heads;
-  attention_step_kernel<T, DP><<<dim3(static_cast<unsigned>(std::min(items, fill)), p.kv_heads), kThreads, L::kTotal, st>>>(p, maps);
-  return cudaGetLastError();
+  const long long items = p.max_slots + static_cast<long long>(p.q_rows) * p.group / kStepRows + p.batch;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kTotal;
+  cfg.stream = st;
+  if (CLUSTER) {
+    cfg.gridDim = dim3(static_cast<unsigned>(items) * kStepCluster, p.kv_heads);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kStepCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  } else {
+    // two CTAs an SM go through the items; no more of them than items
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min(items, (2ll * sms + p.kv_heads - 1) / p.kv_heads)), p.kv_heads);
+  }
+  return cudaLaunchKernelEx(&cfg, attention_step_kernel<T, DP, CLUSTER>, p, maps);
 }
 
 template <class T, int DP>
@@ -443,9 +521,14 @@ namespace svdq {
 
 cudaError_t take_status_attention_step(int* status, cudaStream_t st) { return take_status(status, st); }
 
-cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, int sms, cudaStream_t st) {
-  if (p.dim <= 64) return bf16 ? start<__nv_bfloat16, 64>(p, maps, sms, st) : start<__half, 64>(p, maps, sms, st);
-  return bf16 ? start<__nv_bfloat16, 128>(p, maps, sms, st) : start<__half, 128>(p, maps, sms, st);
+template <class T>
+static cudaError_t start_dim(const AttnParams& p, const AttnMaps& maps, bool cluster, int sms, cudaStream_t st) {
+  if (p.dim <= 64) return cluster ? start<T, 64, true>(p, maps, sms, st) : start<T, 64, false>(p, maps, sms, st);
+  return cluster ? start<T, 128, true>(p, maps, sms, st) : start<T, 128, false>(p, maps, sms, st);
+}
+
+cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, bool cluster, int sms, cudaStream_t st) {
+  return bf16 ? start_dim<__nv_bfloat16>(p, maps, cluster, sms, st) : start_dim<__half>(p, maps, cluster, sms, st);
 }
 
 cudaError_t launch_attention_join(const AttnParams& p, bool bf16, cudaStream_t st) {

@@ -53,12 +53,14 @@ def test_head_dims(dim, dtype, q_lengths):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
-@pytest.mark.parametrize("k_lengths", [[1], [64], [777], [5000, 1, 63, 2047], [0, 20, 0, 9000]])
+@pytest.mark.parametrize("k_lengths", [[1], [64], [777], [5000, 1, 63, 2047], [0, 20, 0, 9000], [30000], [40000, 3, 900],
+                                       [500] * 19 + [0, 1, 3000, 64, 65] * 3])
 def test_single_tokens(k_lengths, dtype):
     check(4, [1] * len(k_lengths), k_lengths, 8, 2, 128, dtype, True)
 
 
-@pytest.mark.parametrize("q_lengths,k_lengths", [([2, 8, 17], [4000, 100, 2500]), ([33], [9001]), ([70, 1], [3000, 8000])])
+@pytest.mark.parametrize("q_lengths,k_lengths", [([2, 8, 17], [4000, 100, 2500]), ([33], [9001]), ([70, 1], [3000, 8000]),
+                                                ([3, 11, 1], [30000, 20000, 50]), ([2] * 30, [100, 1200, 7] * 10)])
 @pytest.mark.parametrize("causal", [False, True])
 def test_pieces_of_long_sequences(q_lengths, k_lengths, causal):
     check(5, q_lengths, k_lengths, 8, 2, 128, BF16, causal)
@@ -81,11 +83,12 @@ def test_queries_that_see_no_key_give_zero(q_lengths, k_lengths):
         at += n
 
 
-@pytest.mark.parametrize("q_lengths", [[1, 1, 1], [150, 300, 70], [20, 20, 20]])
-def test_what_a_query_does_not_see_does_not_reach_it(q_lengths):
+@pytest.mark.parametrize("before", [30, 2500, 20000])
+@pytest.mark.parametrize("q_lengths", [[1, 1, 1], [150, 300, 70], [20, 20, 20], [3, 40, 3]])
+def test_what_a_query_does_not_see_does_not_reach_it(q_lengths, before):
     """Infinities and NaN in the keys and values behind a query and in other sequences; a
     sequence's own last key is seen by its last query, which gets what the definition gives."""
-    k_lengths = [n + 30 for n in q_lengths]
+    k_lengths = [n + before for n in q_lengths]
     q, k, v = make(8, q_lengths, k_lengths, 4, 2, 64, BF16)
     starts = [0, k_lengths[0], k_lengths[0] + k_lengths[1]]
     k[starts[1]:starts[2]] = float("nan")  # the whole middle sequence
@@ -132,30 +135,31 @@ def test_one_sequence_needs_no_offsets():
     assert torch.equal(rq.attention(q[:1], k, v), run(q[:1], k, v, [1], [200], False))
 
 
-@pytest.mark.parametrize("n", [1, 130])
-def test_rows_behind_the_last_sequence_stay(n):
+@pytest.mark.parametrize("n,more", [(1, 0), (130, 0), (1, 30000), (130, 3000)])
+def test_rows_behind_the_last_sequence_stay(n, more):
     import rank_gemm_quantize_b200 as rq
-    q, k, v = make(12, [n, n, n], [500, 20, 80], 4, 2, 64, BF16)
+    q, k, v = make(12, [n, n, n], [500 + more, 20, 80], 4, 2, 64, BF16)
     out = torch.full_like(q, 7.0)
-    o = rq.attention(q, k, v, offsets([n, n]), offsets([500, 20]), causal=True, out=out)
+    o = rq.attention(q, k, v, offsets([n, n]), offsets([500 + more, 20]), causal=True, out=out)
     assert o is out and (out[2 * n:] == 7).all()
-    ops.check(out[:2 * n], *ops.attention(q[:2 * n], k[:520], v[:520], [n, n], [500, 20], True))
+    ops.check(out[:2 * n], *ops.attention(q[:2 * n], k[:520 + more], v[:520 + more], [n, n], [500 + more, 20], True))
 
 
 @pytest.mark.parametrize("bad", [[0, 900, 300], [-5, 20, 1 << 30], [300, 200, 100], [-(1 << 31), (1 << 31) - 1, 7]])
 def test_bad_offsets_stay_inside_the_tensors(bad):
     """Offsets that leave the tensors or run backwards give some result, and the next call is right."""
     import rank_gemm_quantize_b200 as rq
-    for n in (2, 300):
-        q, k, v = make(13, [n], [600], 4, 2, 64, BF16)
+    for n, m in ((2, 600), (2, 40000), (300, 600), (300, 9000)):
+        q, k, v = make(13, [n], [m], 4, 2, 64, BF16)
         o = torch.tensor(bad, dtype=torch.int32).cuda()
         rq.attention(q, k, v, o, o, causal=True)
         torch.cuda.synchronize()
         assert rq.operator_status() == rq.Status.OK
-        ops.check(run(q, k, v, [n], [600], True), *ops.attention(q, k, v, [n], [600], True))
+        ops.check(run(q, k, v, [n], [m], True), *ops.attention(q, k, v, [n], [m], True))
 
 
-@pytest.mark.parametrize("q_lengths,k_lengths", [([1] * 5, [700, 3000, 1, 64, 200]), ([400, 130], [400, 900])])
+@pytest.mark.parametrize("q_lengths,k_lengths", [([1] * 5, [700, 3000, 1, 64, 200]), ([1, 1], [40000, 900]), ([400, 130], [400, 900]),
+                                                ([300], [6000])])
 def test_graph_stream_and_repetition(q_lengths, k_lengths):
     """Captured and replayed on new inputs, on another stream, twice at once, and bit for bit alike."""
     import rank_gemm_quantize_b200 as rq
@@ -181,10 +185,10 @@ def test_graph_stream_and_repetition(q_lengths, k_lengths):
 
 def test_given_workspace_and_its_check():
     import rank_gemm_quantize_b200 as rq
-    q, k, v = make(16, [1, 1], [3000, 900], 4, 2, 64, BF16)
+    q, k, v = make(16, [1, 1], [30000, 900], 4, 2, 64, BF16)
     need = rq.attention_workspace_size(q, k, v, batch=2)
     assert need > 0
-    qo, ko = offsets([1, 1]), offsets([3000, 900])
+    qo, ko = offsets([1, 1]), offsets([30000, 900])
     ws = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device="cuda")
     o = rq.attention(q, k, v, qo, ko, workspace=ws)
     assert torch.equal(o, rq.attention(q, k, v, qo, ko))
