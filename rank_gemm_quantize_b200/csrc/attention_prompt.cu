@@ -4,20 +4,20 @@
 // The query heads of a key head and the queries of a sequence form one list of
 // rows (row = query * group + head), so grouped heads fill the tiles and read
 // each key once. A CTA takes 256 rows of one key head: two tiles of 128
-// rows. Per tile of 128 keys
+// rows. Per 64 keys
 //   S = Q K^T     (both operands in shared memory, S float in tensor memory)
 //   P = 2^(c S - c m), rounded to 16 bits over S in tensor memory
 //   O += P V      (P from tensor memory, V from shared memory as it lies there)
 // with m the row's running maximum and the row's sum kept in registers: one thread
-// owns a row, so neither needs an exchange. While the threads of one tile work on
-// their scores, the tensor core multiplies for the other tile.
+// owns a row, so neither needs an exchange. Each tile has two S: the next one is
+// multiplied while the threads work on the first, so they do not wait for the
+// tensor core (128 keys at a time leave room for one S a tile: 282 us instead).
 //
 // O is not rescaled whenever m grows, only when it grew by more than 2^8 since
 // the last time: P may then be up to 2^8 instead of 1, which costs no digits
 // (its relative rounding is the same), and the final division puts it right.
 //
-// Warps: 0-3 and 4-7 the softmax of the two tiles (224 registers a thread: a
-// whole row of scores), 8 issues the MMAs, 9 the TMA loads, 10 and 11 keep
+// Warps: 0-3 and 4-7 the softmax of the two tiles , 8 issues the MMAs, 9 the TMA loads, 10 and 11 keep
 // values that a query must not see out of the product (below). K and V tiles
 // share one ring of stages in the order K0 V0 K1 V1 ..
 #include <string>
@@ -31,7 +31,8 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kTileRows = 128;
-constexpr int kRegsSoftmax = 224, kRegsOther = 56;  // registers a thread: 256 threads and 128
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;  // registers a thread: 256 threads and 128
+constexpr int kStepN = 64;        // keys of one S
 constexpr float kGrow = 8.f;  // log2 of how far the maximum may grow before O is rescaled
 
 template <int DP>
@@ -50,12 +51,30 @@ __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
   return (piece >> 3) * (128 * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
-// D[tmem] (+)= A[tmem] B: A is 16-bit pairs, one row a lane, 8 columns a k-step of 16.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Operand descriptors of 128-byte-swizzled tiles as two words: the upper is the
+// same for all (8 rows of 128 bytes are 1024 apart), the lower holds the address
+// and the step between columns of 64 values, so a step along a tile is one
+// addition. One thread issues every MMA, and what it does between two of them
+// bounds the kernel (descriptors built anew for each: 135 cycles an MMA).
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | static_cast<uint32_t>(kSw128) << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t column_step) { return saddr >> 4 | (column_step >> 4) << 16; }
+
+// D[tmem] (+)= A B, A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(kDescHigh)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B: A is 16-bit pairs, one row a lane, 8 columns a k-step of 16.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(kDescHigh)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -77,7 +96,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Tensor memory: scores (and, over them, probabilities) of the two tiles, then the two results.
+// A wait of a whole warp. No lane goes ahead before all are through: one that fell
+// behind by two phases would take the wrong one for its own; and all give up, or none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
+
+// Tensor memory: two S (and, over them, P) of each tile, then the two results.
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScoreCol = 0, kResultCol = 256;
 
@@ -88,17 +113,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // [kStages] a K or V tile can be used
   uint64_t* empty = full + L::kStages;                            // [kStages] the MMAs are done with it
-  uint64_t* s_full = empty + L::kStages;                          // [2] a tile's scores are complete
-  uint64_t* p_full = s_full + 2;                                  // [2] its probabilities are written, O is rescaled
-  uint64_t* o_full = p_full + 2;                                  // [2] its result is complete
-  uint64_t* dirty = o_full + 2;                                   // [kStages] a V tile with hidden keys has landed
+  uint64_t* s_full = empty + L::kStages;                          // [2 tiles][2] the scores are complete
+  uint64_t* p_full = s_full + 4;                                  // [2 tiles][2] the probabilities are written, O is rescaled
+  uint64_t* o_full = p_full + 4;                                  // [2 tiles] a product with V is complete
+  uint64_t* o_done = o_full + 2;                                  // [2 tiles] the last one is
+  uint64_t* dirty = o_done + 2;                                   // [kStages] a V tile with hidden keys has landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dirty + L::kStages);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* spoiled = abort_flag + 1;
   __shared__ int sums[kThreads / 32][2];
   __shared__ Found found;
 
-  const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
+  const int tid = threadIdx.x, lane = lane_id();
+  const int warp = __shfl_sync(0xffffffffu, warp_id(), 0);  // known to be the same for the warp
   const int hk = blockIdx.x % p.kv_heads;  // heads side by side: the heaviest tiles of all of them start first
   Search at{0, 0, 0};
   if (!find_item<kThreads / 32>(p, at, blockIdx.x / p.kv_heads, &found, sums)) return;
@@ -113,13 +140,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
   auto limit = [&](int row) {  // the last key a row sees
     return p.causal ? min(row / p.group + kl - ql, kl - 1) : kl - 1;
   };
-  auto key_tiles = [&](int t) {
+  auto key_steps = [&](int t) {
     const int first = row0 + t * kTileRows, last = min(first + kTileRows, rows) - 1;
     if (first >= rows) return 0;
     const int end = min(f.chunks > 1 ? k_begin + p.chunk : kl, limit(last) + 1);
-    return end > k_begin ? (end - k_begin + kPromptKeys - 1) / kPromptKeys : 0;
+    return end > k_begin ? (end - k_begin + kStepN - 1) / kStepN : 0;
   };
-  const int n0 = key_tiles(0), n1 = key_tiles(1), n = max(n0, n1);
+  const int n0 = key_steps(0), n1 = key_steps(1), steps = max(n0, n1);
+  const int n = (steps * kStepN + kPromptKeys - 1) / kPromptKeys;  // key tiles to load
   const int first_limit = limit(row0);
   // key tiles from this one on hold keys that some row does not see
   const int first_hidden = max(0, first_limit + 1 - k_begin) / kPromptKeys;
@@ -134,9 +162,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       mbar_init(&dirty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
       mbar_init(&o_full[t], 1);
+      mbar_init(&o_done[t], 1);
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&p_full[b], 4);
     }
     *abort_flag = 0;
     *spoiled = 0;
@@ -191,58 +222,82 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       }
     } else if (warp == 8) {
       // ------------------------------------------------------------ MMAs
-      if (lane == 0 && n > 0) {
+      // The whole warp goes through the loops, one lane issues: what an MMA reads is
+      // then the same for the warp and stays in uniform registers (a lone lane's
+      // values are moved there for each MMA, 70 cycles of it).
+      if (n > 0) {
         constexpr uint32_t kFmt = Half16<T>::kFmt;
-        const uint32_t idesc_s = idesc_dense(kFmtF32, kFmt, kFmt, kTileRows, kPromptKeys);
+        const uint32_t idesc_s = idesc_dense(kFmtF32, kFmt, kFmt, kTileRows, kStepN);
         const uint32_t idesc_o = idesc_dense(kFmtF32, kFmt, kFmt, kTileRows, DP) | (1u << 16);  // V: columns contiguous
+        const bool issues = elect_one();
+        const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+        const int m0 = __shfl_sync(0xffffffffu, n0, 0), m1 = __shfl_sync(0xffffffffu, n1, 0), all = max(m0, m1);
+        const int tiles = __shfl_sync(0xffffffffu, n, 0);
         const uint32_t q = smem_u32(smem), ring = q + L::kRing;
-        auto wait_full = [&](int i) { return mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1, abort_flag, &g_status); };
-        auto scores = [&](int t, int i) {
-          const uint32_t a = q + t * L::kQTile, b = ring + (i % L::kStages) * L::kStage;
-#pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            const uint32_t at16 = (k >> 2) * (128 * 128) + (k & 3) * 32;
-            mma_f16(tmem + kScoreCol + t * 128, smem_desc(a + at16, 16, 1024, kSw128), smem_desc(b + at16, 16, 1024, kSw128), idesc_s, k > 0);
-          }
-          tc_commit(&s_full[t]);
+        auto wait_full = [&](int i) { return warp_wait(&full[i % L::kStages], (i / L::kStages) & 1, abort_flag, &g_status); };
+        auto buffer = [&](int t, int u) { return 2 * t + (u & 1); };
+        auto commit = [&](uint64_t* bar) {
+          if (issues) tc_commit(bar);
         };
-        auto products = [&](int t, int i, bool first) {
-          const uint32_t b = ring + (i % L::kStages) * L::kStage;
+        auto scores = [&](int t, int u) {  // keys 64 u .. of K tile u / 2
+          const int i = 2 * (u >> 1);
+          const uint32_t a = desc_low(q + t * L::kQTile, 16);
+          const uint32_t b = desc_low(ring + (i % L::kStages) * L::kStage + (u & 1) * (kStepN * 128), 16);
+          const uint32_t d = base + kScoreCol + buffer(t, u) * kStepN;
+          if (issues) {
 #pragma unroll
-          for (int k = 0; k < kPromptKeys / 16; ++k)
-            mma_f16_ts(tmem + kResultCol + t * DP, tmem + kScoreCol + t * 128 + 8 * k, smem_desc(b + 2048 * k, 128 * 128, 1024, kSw128),
-                       idesc_o, !first || k > 0);
+            for (int k = 0; k < DP / 16; ++k) {
+              const uint32_t at16 = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+              mma_ss(d, a + at16, b + at16, idesc_s, k > 0);
+            }
+            tc_commit(&s_full[buffer(t, u)]);
+          }
+        };
+        auto products = [&](int t, int u) {
+          const int i = 2 * (u >> 1) + 1;
+          const uint32_t b = desc_low(ring + (i % L::kStages) * L::kStage + (u & 1) * (kStepN * 128), 128 * 128);
+          const uint32_t d = base + kResultCol + t * DP, a = base + kScoreCol + buffer(t, u) * kStepN;
+          if (issues) {
+#pragma unroll
+            for (int k = 0; k < kStepN / 16; ++k) mma_ts(d, a + 8 * k, b + (2048 >> 4) * k, idesc_o, u > 0 || k > 0);
+            tc_commit(&o_full[t]);
+          }
         };
         bool ok = wait_full(0);
         if (ok) {
           tc_fence_after();
-          if (n0 > 0) scores(0, 0);
-          if (n1 > 0) scores(1, 0);
-          tc_commit(&empty[0]);
+          for (int u = 0; u < 2; ++u) {
+            if (u < m0) scores(0, u);
+            if (u < m1) scores(1, u);
+          }
+          commit(&empty[0]);
         }
-        for (int j = 0; j < n && ok; ++j) {
-          const int iv = 2 * j + 1, ik = 2 * j + 2;
-          ok = wait_full(iv);
-          if (ok && j + 1 < n) ok = wait_full(ik);
-          for (int t = 0; t < 2 && ok; ++t) {
-            const int nt = t ? n1 : n0;
-            if (j >= nt) continue;
-            ok = mbar_wait(&p_full[t], j & 1, abort_flag, &g_status);
-            if (!ok) break;
+        for (int u = 0; u < all && ok; ++u) {
+          const int iv = 2 * (u >> 1) + 1, ik = iv + 1;  // V tile of step u, K tile of step u + 2
+          if (!(u & 1)) {
+            ok = wait_full(iv);
+            if (ok && u + 2 < all) ok = wait_full(ik);
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int nt = t ? m1 : m0;
+            if (!ok || u >= nt) continue;
+            ok = warp_wait(&p_full[buffer(t, u)], (u >> 1) & 1, abort_flag, &g_status);
+            if (!ok) continue;
             tc_fence_after();
-            products(t, iv, j == 0);
-            if (j + 1 < nt)
-              scores(t, ik);  // over P: MMAs of one thread run in order
-            else
-              tc_commit(&o_full[t]);
+            products(t, u);
+            if (u + 2 < nt) scores(t, u + 2);  // over P: MMAs of one thread run in order
+            if (u + 1 == nt) commit(&o_done[t]);
           }
           if (!ok) break;
-          tc_commit(&empty[iv % L::kStages]);
-          if (j + 1 < n) tc_commit(&empty[ik % L::kStages]);
+          if (u & 1) {  // both halves of the tiles are used
+            commit(&empty[iv % L::kStages]);
+            if (ik < 2 * tiles) commit(&empty[ik % L::kStages]);
+          }
         }
         if (!ok) {  // gave up: the MMAs in flight end before the CTA does
-          tc_commit(&o_full[0]);
-          tc_commit(&o_full[1]);
+          commit(&o_done[0]);
+          commit(&o_done[1]);
         }
       }
     } else {
@@ -253,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       // and are put back into the rows that do see them at the end.
       for (int j = first_hidden; j < n; ++j) {
         const int stage = (2 * j + 1) % L::kStages;
-        if (!mbar_wait(&dirty[stage], hidden_parity(j), abort_flag, &g_status)) break;
+        if (!warp_wait(&dirty[stage], hidden_parity(j), abort_flag, &g_status)) break;
         uint8_t* st = smem + L::kRing + stage * L::kStage;
         const int key0 = k_begin + j * kPromptKeys;
         bool any = false;
@@ -278,26 +333,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
     // -------------------------------------------------------------- softmax
     const int t = warp >> 2, nt = t ? n1 : n0;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t scores = tmem + lanes + kScoreCol + t * 128, result = tmem + lanes + kResultCol + t * DP;
+    const uint32_t result = tmem + lanes + kResultCol + t * DP;
     const int row = row0 + t * kTileRows + 32 * (warp & 3) + lane;
     const int lim = row < rows ? limit(row) : -1;
     const int warp_limit = limit(row - lane);  // its first row sees least
     const float c = p.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < nt; ++j) {
-      ok = mbar_wait(&s_full[t], j & 1, abort_flag, &g_status);
+    for (int u = 0; u < nt; ++u) {
+      const uint32_t scores = tmem + lanes + kScoreCol + (2 * t + (u & 1)) * kStepN;
+      ok = warp_wait(&s_full[2 * t + (u & 1)], (u >> 1) & 1, abort_flag, &g_status);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[4][32];
+      uint32_t s[2][32];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) tmem_ld32(scores + 32 * b, s[b]);
+      for (int b = 0; b < 2; ++b) tmem_ld32(scores + 32 * b, s[b]);
       tmem_ld_wait();
-      const int key0 = k_begin + j * kPromptKeys;
-      if (key0 + kPromptKeys - 1 > warp_limit) {
+      const int key0 = k_begin + u * kStepN;
+      if (key0 + kStepN - 1 > warp_limit) {
         const int seen = lim - key0;
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (32 * b + e > seen) s[b][e] = 0xFF800000u;  // minus infinity
@@ -305,9 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       float top[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        top[b] = __uint_as_float(s[b][0]);
+        top[b] = __uint_as_float(s[b >> 1][16 * (b & 1)]);
 #pragma unroll
-        for (int e = 1; e < 32; ++e) top[b] = fmaxf(top[b], __uint_as_float(s[b][e]));
+        for (int e = 1; e < 16; ++e) top[b] = fmaxf(top[b], __uint_as_float(s[b >> 1][16 * (b & 1) + e]));
       }
       const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
       const bool grew = (now - m) * c > kGrow;  // also the first time; false while nothing was seen
@@ -315,7 +371,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
         const float factor = grew ? exp2_fast((m - now) * c) : 1.f;
         if (grew) m = now;
         l *= factor;
-        if (j > 0) {  // the last product is complete: these scores were issued after it
+        if (u > 0) {
+          // The last product has to be complete. The one before it is, as these scores were
+          // issued after it, and the next waits for this warp: the parity is unambiguous.
+          ok = warp_wait(&o_full[t], (u - 1) & 1, abort_flag, &g_status);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
           for (int b = 0; b < DP; b += 32) {
             uint32_t o[32];
@@ -331,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       const float2 c2 = make_float2(c, c), base2 = make_float2(-base, -base);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
+      for (int b = 0; b < 2; ++b) {
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -347,11 +408,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t]);
+      if (lane == 0) mbar_arrive(&p_full[2 * t + (u & 1)]);
     }
     if (nt > 0) {
       volatile int no_abort = 0;
-      ok = mbar_wait(&o_full[t], 0, &no_abort, &g_status) && ok && !*abort_flag;
+      ok = warp_wait(&o_done[t], 0, &no_abort, &g_status) && ok && __all_sync(0xffffffffu, !*abort_flag);
       tc_fence_after();
     }
     // ---------------------------------------------------------------- result
@@ -361,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       const int share = f.slots + tile * f.chunks + f.chunk;
       const size_t slot = (static_cast<size_t>(share) * p.kv_heads + hk) * kPromptRows + row - row0;
       const bool write = row < rows && (!split || share < p.max_slots);
-      const int spoil_end = *spoiled ? min(lim + 1, k_begin + nt * kPromptKeys) : 0;
+      const int spoil_end = *spoiled ? min(lim + 1, k_begin + nt * kStepN) : 0;
       T* out = static_cast<T*>(p.out) + (static_cast<size_t>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim;
 #pragma unroll 1
       for (int b = 0; b < DP; b += 32) {
@@ -373,28 +434,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        if (!write) continue;
-        for (int key = max(k_begin, first_limit + 1); key < spoil_end; ++key) {
-          const T* v = static_cast<const T*>(p.v) + static_cast<long long>(ks + key) * p.v_row + hk * p.v_head + b;
+        __syncwarp();  // the next load of tensor memory takes the whole warp
+        if (write) {
+          for (int key = max(k_begin, first_limit + 1); key < spoil_end; ++key) {
+            const T* v = static_cast<const T*>(p.v) + static_cast<long long>(ks + key) * p.v_row + hk * p.v_head + b;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const uint32_t bits = b + e < p.dim ? reinterpret_cast<const uint16_t*>(v)[e] : 0u;
-            if ((bits & Half16<T>::kExp) == Half16<T>::kExp) o[e] = __float_as_uint(__uint_as_float(o[e]) + Half16<T>::to_float(bits));
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t bits = b + e < p.dim ? reinterpret_cast<const uint16_t*>(v)[e] : 0u;
+              if ((bits & Half16<T>::kExp) == Half16<T>::kExp) o[e] = __float_as_uint(__uint_as_float(o[e]) + Half16<T>::to_float(bits));
+            }
+          }
+          if (split) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(p.part + slot * DP + b + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) w[h] = Half16<T>::pack(__uint_as_float(o[e + 2 * h]) * norm, __uint_as_float(o[e + 2 * h + 1]) * norm);
+              if (b + e < p.dim) *reinterpret_cast<uint4*>(out + b + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
         }
-        if (split) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(p.part + slot * DP + b + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) w[h] = Half16<T>::pack(__uint_as_float(o[e + 2 * h]) * norm, __uint_as_float(o[e + 2 * h + 1]) * norm);
-            if (b + e < p.dim) *reinterpret_cast<uint4*>(out + b + e) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
+        __syncwarp();
       }
       if (split && write) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(m, l);
     }
