@@ -4,14 +4,22 @@
 // The query heads of a key head and the queries of a sequence form one list of
 // rows (row = query * group + head), so grouped heads fill the tiles and read
 // each key once. A CTA takes 256 rows of one key head: two tiles of 128
-// rows. Per 64 keys
+// rows. Per 128 keys
 //   S = Q K^T     (both operands in shared memory, S float in tensor memory)
 //   P = 2^(c S - c m), rounded to 16 bits over S in tensor memory
 //   O += P V      (P from tensor memory, V from shared memory as it lies there)
 // with m the row's running maximum and the row's sum kept in registers: one thread
-// owns a row, so neither needs an exchange. Each tile has two S: the next one is
-// multiplied while the threads work on the first, so they do not wait for the
-// tensor core (128 keys at a time leave room for one S a tile: 282 us instead).
+// owns a row, so neither needs an exchange. While the threads of one tile work on
+// their scores, the tensor core multiplies for the other tile; P goes to it in
+// two halves, so that the first is multiplied while the second is computed.
+//
+// A tile's chain of S, softmax and P V is what has to be short: the two tiles'
+// products take 2048 cycles per 128 keys, the softmax may take as long as one
+// tile's. The exponential unit alone would need 1024 cycles a tile, so three
+// of eight exponentials are computed with multiply-adds (exp2_pair).
+// (Two S of 64 keys a tile would shorten the chain, but an MMA of 64 columns takes
+// as long as one of 128: 302 us where this takes KERNEL us, 4608 x 4608 keys,
+// 24 heads of 128.)
 //
 // O is not rescaled whenever m grows, only when it grew by more than 2^8 since
 // the last time: P may then be up to 2^8 instead of 1, which costs no digits
@@ -21,6 +29,7 @@
 // values that a query must not see out of the product (below). K and V tiles
 // share one ring of stages in the order K0 V0 K1 V1 ..
 #include <string>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "operator_status.cuh"
@@ -31,8 +40,8 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kTileRows = 128;
-constexpr int kRegsSoftmax = 200, kRegsOther = 104;  // registers a thread: 256 threads and 128
-constexpr int kStepN = 64;        // keys of one S
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;  // registers a thread: 256 threads and 128
+constexpr int kStepN = 128;       // keys of one S
 constexpr float kGrow = 8.f;  // log2 of how far the maximum may grow before O is rescaled
 
 template <int DP>
@@ -102,7 +111,25 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
 }
 
-// Tensor memory: two S (and, over them, P) of each tile, then the two results.
+// 2^x of two values without the exponential unit: x = i + f, f in [-1/2, 1/2]; the
+// polynomial (minimax in the relative error by Lawson's iteration, 2.6e-6) gives
+// 2^f, and i goes into its exponent. Below -127 as at -127; NaN stays.
+__device__ __forceinline__ float2 exp2_pair(float2 x) {
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
+  auto both = [](float c) { return make_float2(c, c); };
+  const float2 t = __fadd2_rn(x, both(12582912.f));  // 3 2^22: i in the low bits
+  const float2 f = __ffma2_rn(__fadd2_rn(t, both(-12582912.f)), both(-1.f), x);
+  float2 q = both(0.00957007046f);
+  q = __ffma2_rn(q, f, both(0.0559178127f));
+  q = __ffma2_rn(q, f, both(0.240247451f));
+  q = __ffma2_rn(q, f, both(0.693121821f));
+  q = __ffma2_rn(q, f, both(0.999999262f));
+  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// Tensor memory: S (and, over it, P) of the two tiles, then the two results.
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScoreCol = 0, kResultCol = 256;
 
@@ -113,10 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // [kStages] a K or V tile can be used
   uint64_t* empty = full + L::kStages;                            // [kStages] the MMAs are done with it
-  uint64_t* s_full = empty + L::kStages;                          // [2 tiles][2] the scores are complete
-  uint64_t* p_full = s_full + 4;                                  // [2 tiles][2] the probabilities are written, O is rescaled
-  uint64_t* o_full = p_full + 4;                                  // [2 tiles] a product with V is complete
-  uint64_t* o_done = o_full + 2;                                  // [2 tiles] the last one is
+  uint64_t* s_full = empty + L::kStages;                          // [2 tiles] the scores are complete
+  uint64_t* p_full = s_full + 2;                                  // [2 tiles][2] a half of the probabilities is written
+  uint64_t* o_done = p_full + 4;                                  // [2 tiles] the last product with V is complete
   uint64_t* dirty = o_done + 2;                                   // [kStages] a V tile with hidden keys has landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dirty + L::kStages);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -162,13 +188,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       mbar_init(&dirty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&o_full[t], 1);
+      mbar_init(&s_full[t], 1);
       mbar_init(&o_done[t], 1);
     }
-    for (int b = 0; b < 4; ++b) {
-      mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], 4);
-    }
+    for (int h = 0; h < 4; ++h) mbar_init(&p_full[h], 4);
     *abort_flag = 0;
     *spoiled = 0;
     fence_barrier_init();
@@ -232,68 +255,62 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
         const bool issues = elect_one();
         const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
         const int m0 = __shfl_sync(0xffffffffu, n0, 0), m1 = __shfl_sync(0xffffffffu, n1, 0), all = max(m0, m1);
-        const int tiles = __shfl_sync(0xffffffffu, n, 0);
         const uint32_t q = smem_u32(smem), ring = q + L::kRing;
         auto wait_full = [&](int i) { return warp_wait(&full[i % L::kStages], (i / L::kStages) & 1, abort_flag, &g_status); };
-        auto buffer = [&](int t, int u) { return 2 * t + (u & 1); };
         auto commit = [&](uint64_t* bar) {
           if (issues) tc_commit(bar);
         };
-        auto scores = [&](int t, int u) {  // keys 64 u .. of K tile u / 2
-          const int i = 2 * (u >> 1);
-          const uint32_t a = desc_low(q + t * L::kQTile, 16);
-          const uint32_t b = desc_low(ring + (i % L::kStages) * L::kStage + (u & 1) * (kStepN * 128), 16);
-          const uint32_t d = base + kScoreCol + buffer(t, u) * kStepN;
+        auto scores = [&](int t, int j) {
+          const uint32_t a = desc_low(q + t * L::kQTile, 16), b = desc_low(ring + (2 * j) % L::kStages * L::kStage, 16);
+          const uint32_t d = base + kScoreCol + t * kStepN;
           if (issues) {
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k) {
               const uint32_t at16 = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
               mma_ss(d, a + at16, b + at16, idesc_s, k > 0);
             }
-            tc_commit(&s_full[buffer(t, u)]);
+            tc_commit(&s_full[t]);
           }
         };
-        auto products = [&](int t, int u) {
-          const int i = 2 * (u >> 1) + 1;
-          const uint32_t b = desc_low(ring + (i % L::kStages) * L::kStage + (u & 1) * (kStepN * 128), 128 * 128);
-          const uint32_t d = base + kResultCol + t * DP, a = base + kScoreCol + buffer(t, u) * kStepN;
+        auto products = [&](int t, int j, int half) {  // 64 of the tile's keys
+          const uint32_t b = desc_low(ring + (2 * j + 1) % L::kStages * L::kStage + half * (64 * 128), 128 * 128);
+          const uint32_t d = base + kResultCol + t * DP, a = base + kScoreCol + t * kStepN + half * 32;
           if (issues) {
 #pragma unroll
-            for (int k = 0; k < kStepN / 16; ++k) mma_ts(d, a + 8 * k, b + (2048 >> 4) * k, idesc_o, u > 0 || k > 0);
-            tc_commit(&o_full[t]);
+            for (int k = 0; k < 4; ++k) mma_ts(d, a + 8 * k, b + (2048 >> 4) * k, idesc_o, j > 0 || half > 0 || k > 0);
           }
         };
         bool ok = wait_full(0);
         if (ok) {
           tc_fence_after();
-          for (int u = 0; u < 2; ++u) {
-            if (u < m0) scores(0, u);
-            if (u < m1) scores(1, u);
-          }
+          if (m0 > 0) scores(0, 0);
+          if (m1 > 0) scores(1, 0);
           commit(&empty[0]);
         }
-        for (int u = 0; u < all && ok; ++u) {
-          const int iv = 2 * (u >> 1) + 1, ik = iv + 1;  // V tile of step u, K tile of step u + 2
-          if (!(u & 1)) {
-            ok = wait_full(iv);
-            if (ok && u + 2 < all) ok = wait_full(ik);
-          }
+        for (int j = 0; j < all && ok; ++j) {
+          const int iv = 2 * j + 1, ik = iv + 1;  // V tile of this step, K tile of the next
+          ok = wait_full(iv);
+          if (ok && j + 1 < all) ok = wait_full(ik);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int nt = t ? m1 : m0;
-            if (!ok || u >= nt) continue;
-            ok = warp_wait(&p_full[buffer(t, u)], (u >> 1) & 1, abort_flag, &g_status);
+            if (!ok || j >= nt) continue;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (ok) ok = warp_wait(&p_full[2 * t + half], j & 1, abort_flag, &g_status);
+              if (!ok) continue;
+              tc_fence_after();
+              products(t, j, half);
+            }
             if (!ok) continue;
-            tc_fence_after();
-            products(t, u);
-            if (u + 2 < nt) scores(t, u + 2);  // over P: MMAs of one thread run in order
-            if (u + 1 == nt) commit(&o_done[t]);
+            if (j + 1 < nt)
+              scores(t, j + 1);  // over P: MMAs of one thread run in order
+            else
+              commit(&o_done[t]);
           }
           if (!ok) break;
-          if (u & 1) {  // both halves of the tiles are used
-            commit(&empty[iv % L::kStages]);
-            if (ik < 2 * tiles) commit(&empty[ik % L::kStages]);
-          }
+          commit(&empty[iv % L::kStages]);
+          if (j + 1 < all) commit(&empty[ik % L::kStages]);
         }
         if (!ok) {  // gave up: the MMAs in flight end before the CTA does
           commit(&o_done[0]);
@@ -340,20 +357,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
     const float c = p.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int u = 0; u < nt; ++u) {
-      const uint32_t scores = tmem + lanes + kScoreCol + (2 * t + (u & 1)) * kStepN;
-      ok = warp_wait(&s_full[2 * t + (u & 1)], (u >> 1) & 1, abort_flag, &g_status);
+    const uint32_t scores = tmem + lanes + kScoreCol + t * kStepN;
+    for (int j = 0; j < nt; ++j) {
+      ok = warp_wait(&s_full[t], j & 1, abort_flag, &g_status);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[2][32];
+      uint32_t s[4][32];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) tmem_ld32(scores + 32 * b, s[b]);
+      for (int b = 0; b < 4; ++b) tmem_ld32(scores + 32 * b, s[b]);
       tmem_ld_wait();
-      const int key0 = k_begin + u * kStepN;
-      if (key0 + kStepN - 1 > warp_limit) {
+      const int key0 = k_begin + j * kStepN;
+      const bool masked = key0 + kStepN - 1 > warp_limit;  // some row does not see some key
+      if (masked) {
         const int seen = lim - key0;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 4; ++b)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (32 * b + e > seen) s[b][e] = 0xFF800000u;  // minus infinity
@@ -361,9 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       float top[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        top[b] = __uint_as_float(s[b >> 1][16 * (b & 1)]);
+        top[b] = fmaxf(__uint_as_float(s[b][0]), __uint_as_float(s[b][1]));
 #pragma unroll
-        for (int e = 1; e < 16; ++e) top[b] = fmaxf(top[b], __uint_as_float(s[b >> 1][16 * (b & 1) + e]));
+        for (int e = 2; e < 32; e += 2) top[b] = fmaxf(fmaxf(top[b], __uint_as_float(s[b][e])), __uint_as_float(s[b][e + 1]));
       }
       const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
       const bool grew = (now - m) * c > kGrow;  // also the first time; false while nothing was seen
@@ -371,12 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
         const float factor = grew ? exp2_fast((m - now) * c) : 1.f;
         if (grew) m = now;
         l *= factor;
-        if (u > 0) {
-          // The last product has to be complete. The one before it is, as these scores were
-          // issued after it, and the next waits for this warp: the parity is unambiguous.
-          ok = warp_wait(&o_full[t], (u - 1) & 1, abort_flag, &g_status);
-          if (!ok) break;
-          tc_fence_after();
+        if (j > 0) {  // the last product is complete: these scores were issued after it
 #pragma unroll
           for (int b = 0; b < DP; b += 32) {
             uint32_t o[32];
@@ -391,24 +404,38 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       const float base = (m == -INFINITY ? 0.f : m) * c;
       const float2 c2 = make_float2(c, c), base2 = make_float2(-base, -base);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      // MIXED: three of eight pairs by multiply-adds, where no key is hidden (those need 0 exactly)
+      auto half = [&](int h, auto mixed) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        uint32_t pk[16];
+        for (int b = 2 * h; b < 2 * h + 2; ++b) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 x = __ffma2_rn(make_float2(__uint_as_float(s[b][2 * e]), __uint_as_float(s[b][2 * e + 1])), c2, base2);
-          x.x = exp2_fast(x.x);
-          x.y = exp2_fast(x.y);
-          sum[e & 1] = __fadd2_rn(sum[e & 1], x);
-          pk[e] = Half16<T>::pack(x.x, x.y);
+          for (int e = 0; e < 16; ++e) {
+            float2 x = __ffma2_rn(make_float2(__uint_as_float(s[b][2 * e]), __uint_as_float(s[b][2 * e + 1])), c2, base2);
+            if (decltype(mixed)::value && (3 * e) % 8 < 3) {
+              x = exp2_pair(x);
+            } else {
+              x.x = exp2_fast(x.x);
+              x.y = exp2_fast(x.y);
+            }
+            sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+            pk[e] = Half16<T>::pack(x.x, x.y);
+          }
+          tmem_st16(scores + 16 * b, pk);
         }
-        tmem_st16(scores + 16 * b, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
+      };
+      if (masked) {
+        half(0, std::false_type());
+        half(1, std::false_type());
+      } else {
+        half(0, std::true_type());
+        half(1, std::true_type());
       }
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[2 * t + (u & 1)]);
     }
     if (nt > 0) {
       volatile int no_abort = 0;
