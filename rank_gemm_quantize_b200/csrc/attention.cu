@@ -50,6 +50,8 @@ struct Plan {
   int sms, chunk, max_slots;
   bool prompt;   // attention_prompt.cu, or attention_step.cu
   bool cluster;  // attention_step.cu: an item's shares are a cluster
+  bool open;     // attention_prompt.cu: the kernel sets `chunk`
+  int fill;
   size_t ml, total;
 };
 
@@ -67,11 +69,15 @@ svdq_status plan(const svdq_attention_config* c, Plan* out) {
   p.prompt = rows > 64ll * c->batch;
   const int key_tile = p.prompt ? kPromptKeys : kStepKeys, tile_rows = p.prompt ? kPromptRows : kStepRows;
   long long keys, tiles;  // keys of a share; row tiles that can have several shares
+  long long slots = -1;
   if (p.prompt) {
-    // cut the keys only where the row tiles leave SMs idle, into no less than 512 of them
-    tiles = rows / kPromptRows + c->batch;
-    const long long shares = p.sms / (tiles * c->kv_heads);
-    keys = shares > 1 ? std::max<long long>(512, c->k_rows / shares) : c->k_rows;
+    // where the row tiles alone leave SMs idle, the kernel cuts the keys (key_chunk);
+    // its shares are no more than the CTAs that run at once
+    tiles = rows / kPromptRows;
+    p.fill = p.sms / c->kv_heads;
+    p.open = c->batch <= 32 && tiles < p.fill && c->k_rows > 768;  // of fewer keys no share would have 512
+    keys = c->k_rows;
+    slots = p.open ? p.fill : 0;
   } else if ((rows / kStepRows + c->batch) * c->kv_heads * kStepCluster <= 2 * p.sms &&
              c->k_rows <= static_cast<long long>(1024) * kStepCluster * c->batch) {
     // all clusters run at once, and their shares of the keys are short
@@ -86,7 +92,7 @@ svdq_status plan(const svdq_attention_config* c, Plan* out) {
   }
   p.chunk = static_cast<int>(std::max<long long>(1, (keys + key_tile - 1) / key_tile) * key_tile);
   // a sequence of more than `chunk` keys has fewer than 2 keys / chunk shares
-  const long long slots = c->k_rows > p.chunk ? 2ll * c->k_rows / p.chunk * tiles : 0;
+  if (slots < 0) slots = c->k_rows > p.chunk ? 2ll * c->k_rows / p.chunk * tiles : 0;
   if ((slots + rows / tile_rows + c->batch) * c->kv_heads > 0x7fffffffll) return fail(SVDQ_ERR_UNSUPPORTED, "too many sequences times heads");
   p.max_slots = static_cast<int>(slots);
   const size_t slot_rows = static_cast<size_t>(slots) * c->kv_heads * tile_rows;
@@ -154,7 +160,8 @@ svdq_status svdq_attention_forward(const svdq_attention_config* cfg, const void*
   p.v_head = cfg->v_head_stride;
   p.tile_rows = pl.prompt ? kPromptRows : kStepRows;
   p.split_tiles = pl.prompt ? INT_MAX : kStepSplitTiles;
-  p.chunk = pl.chunk;
+  p.chunk = pl.open ? 0 : pl.chunk;
+  p.fill = pl.fill;
   p.max_slots = pl.max_slots;
   p.part = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.ml);

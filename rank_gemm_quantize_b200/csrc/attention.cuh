@@ -15,9 +15,10 @@ struct AttnParams {
   float scale_log2;   // scale * log2(e): softmax in base 2
   long long q_row, q_head, v_row, v_head;  // strides in elements
   // A sequence's rows (query * group + head in the group) are cut into tiles of
-  // tile_rows, its keys into shares of `chunk` (a multiple of the key tile) where
-  // it has at most split_tiles row tiles.
+  // tile_rows, its keys into shares of `chunk` (a multiple of the key tile; 0: see
+  // key_chunk) where it has at most split_tiles row tiles.
   int tile_rows, split_tiles, chunk;
+  int fill;           // with chunk 0: CTAs a key head that run at once
   int max_slots;      // partial results (tile_rows rows each) the workspace holds
   float *part, *part_ml;
 };
@@ -93,13 +94,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
 struct Shares {
   int tiles, chunks, slots;
 };
-__device__ __forceinline__ Shares shares_of(const AttnParams& p, int b) {
+__device__ __forceinline__ Shares shares_of(const AttnParams& p, int b, int chunk) {
   int qs, ql, ks, kl;
   seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
   seq_extent(p.k_offsets, b, p.k_rows, ks, kl);
   Shares s;
   s.tiles = (ql * p.group + p.tile_rows - 1) / p.tile_rows;
-  s.chunks = s.tiles <= p.split_tiles && kl > p.chunk ? (kl + p.chunk - 1) / p.chunk : 1;
+  s.chunks = s.tiles <= p.split_tiles && kl > chunk ? (kl + chunk - 1) / chunk : 1;
   s.slots = s.chunks > 1 ? s.tiles * s.chunks : 0;
   return s;
 }
@@ -113,22 +114,71 @@ __device__ __forceinline__ int warp_inclusive(int v) {
   return v;
 }
 
+// The keys of a share where the host left it open (few row tiles, up to 32
+// sequences): the longest sequence's keys cut into as many shares as still run at
+// once, each of 512 keys or more. The lengths are on the device, so every CTA
+// works it out for itself, and all come to the same.
+constexpr int kAutoShares = 16;
+__device__ __forceinline__ int key_chunk(const AttnParams& p) {
+  if (p.chunk) return p.chunk;
+  const int lane = lane_id();
+  int tiles = 0, keys = 0;
+  if (lane < p.batch) {
+    int start, ql;
+    seq_extent(p.q_offsets, lane, p.q_rows, start, ql);
+    seq_extent(p.k_offsets, lane, p.k_rows, start, keys);
+    tiles = (ql * p.group + p.tile_rows - 1) / p.tile_rows;
+    if (!tiles) keys = 0;
+  }
+  int longest = keys;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  int chunk = longest + 1;
+  for (int n = 2; n <= kAutoShares; ++n) {
+    const int c = ((longest + n - 1) / n + 127) & ~127;
+    int ctas = tiles * (keys > c ? (keys + c - 1) / c : 1);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ctas += __shfl_xor_sync(0xffffffffu, ctas, o);
+    if (c < 512 || ctas > p.fill) break;
+    chunk = c;
+  }
+  return chunk;
+}
+
 struct Found {
   int b, tile, tiles, chunk, chunks;
   int slots;  // workspace slots before the sequence's; it has slot tile * chunks + chunk of its own
 };
 struct Search {  // where the search for an item stands: sequences before b0 hold `items` items and `slots` slots
   int b0, items, slots;
+  int chunk;  // key_chunk
 };
 
 // The sequence, row tile and key share of item `idx`: false behind the last.
-// Called by the whole CTA of WARPS warps with idx that never decreases.
+// Called by the whole CTA of WARPS warps with idx that never decreases; `shared`
+// and `sums` are in shared memory.
 template <int WARPS>
-__device__ bool find_item(const AttnParams& p, Search& at, int idx, Found* found, int (*sums)[2]) {
+__device__ bool find_item(const AttnParams& p, Search& at, int idx, Found* shared, int (*sums)[2], Found* found) {
+  if (p.batch <= 32) {  // each warp for itself, no barrier
+    const int lane = lane_id();
+    Shares s{0, 0, 0};
+    if (lane < p.batch) s = shares_of(p, lane, at.chunk);
+    const int own = s.tiles * s.chunks, items = warp_inclusive(own), slots = warp_inclusive(s.slots);
+    const unsigned here = __ballot_sync(0xffffffffu, idx >= items - own && idx < items);
+    if (!here) return false;
+    const int b = __ffs(here) - 1, i = idx - (__shfl_sync(0xffffffffu, items - own, b));
+    found->b = b;
+    found->tiles = __shfl_sync(0xffffffffu, s.tiles, b);
+    found->chunks = __shfl_sync(0xffffffffu, s.chunks, b);
+    found->slots = __shfl_sync(0xffffffffu, slots - s.slots, b);
+    found->tile = i / found->chunks;
+    found->chunk = i % found->chunks;
+    return true;
+  }
   for (; at.b0 < p.batch; at.b0 += WARPS * 32) {
     const int b = at.b0 + static_cast<int>(threadIdx.x);
     Shares s{0, 0, 0};
-    if (b < p.batch) s = shares_of(p, b);
+    if (b < p.batch) s = shares_of(p, b, at.chunk);
     const int own = s.tiles * s.chunks;
     int items = warp_inclusive(own), slots = warp_inclusive(s.slots);
     __syncthreads();  // the previous use of sums and found is over
@@ -148,14 +198,15 @@ __device__ bool find_item(const AttnParams& p, Search& at, int idx, Found* found
       const int first = at.items + items - own;
       if (idx >= first && idx < first + own) {
         const int i = idx - first;
-        found->b = b;
-        found->tile = i / s.chunks;
-        found->tiles = s.tiles;
-        found->chunk = i % s.chunks;
-        found->chunks = s.chunks;
-        found->slots = at.slots + slots - s.slots;
+        shared->b = b;
+        shared->tile = i / s.chunks;
+        shared->tiles = s.tiles;
+        shared->chunk = i % s.chunks;
+        shared->chunks = s.chunks;
+        shared->slots = at.slots + slots - s.slots;
       }
       __syncthreads();
+      *found = *shared;
       return true;
     }
     at.items += total_items;

@@ -93,16 +93,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
-      "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A wait of a whole warp. No lane goes ahead before all are through: one that fell
@@ -153,23 +143,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
   const int tid = threadIdx.x, lane = lane_id();
   const int warp = __shfl_sync(0xffffffffu, warp_id(), 0);  // known to be the same for the warp
   const int hk = blockIdx.x % p.kv_heads;  // heads side by side: the heaviest tiles of all of them start first
-  Search at{0, 0, 0};
-  if (!find_item<kThreads / 32>(p, at, blockIdx.x / p.kv_heads, &found, sums)) return;
-  const Found f = found;
+  Search at{0, 0, 0, key_chunk(p)};
+  Found f;
+  if (!find_item<kThreads / 32>(p, at, blockIdx.x / p.kv_heads, &found, sums, &f)) return;
   int qs, ql, ks, kl;
   seq_extent(p.q_offsets, f.b, p.q_rows, qs, ql);
   seq_extent(p.k_offsets, f.b, p.k_rows, ks, kl);
   const int rows = ql * p.group;
   // the tiles that see most keys first
   const int tile = f.tiles - 1 - f.tile, row0 = tile * kPromptRows;
-  const int k_begin = f.chunks > 1 ? f.chunk * p.chunk : 0;
+  const int k_begin = f.chunks > 1 ? f.chunk * at.chunk : 0;
   auto limit = [&](int row) {  // the last key a row sees
     return p.causal ? min(row / p.group + kl - ql, kl - 1) : kl - 1;
   };
   auto key_steps = [&](int t) {
     const int first = row0 + t * kTileRows, last = min(first + kTileRows, rows) - 1;
     if (first >= rows) return 0;
-    const int end = min(f.chunks > 1 ? k_begin + p.chunk : kl, limit(last) + 1);
+    const int end = min(f.chunks > 1 ? k_begin + at.chunk : kl, limit(last) + 1);
     return end > k_begin ? (end - k_begin + kStepN - 1) / kStepN : 0;
   };
   const int n0 = key_steps(0), n1 = key_steps(1), steps = max(n0, n1);
@@ -181,7 +171,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
   constexpr int kPeriod = L::kStages % 2 ? L::kStages : L::kStages / 2;
   auto hidden_parity = [&](int j) { return static_cast<uint32_t>((j - first_hidden) / kPeriod & 1); };
 
-  if (tid == 0) {
+  // loads: K of key tile i / 2, then its V
+  auto hidden = [&](int i) { return (i & 1) && (i >> 1) >= first_hidden; };
+  auto load = [&](int i) {
+    const int s = i % L::kStages;
+    uint8_t* st = smem + L::kRing + s * L::kStage;
+    const CUtensorMap* map = i & 1 ? &maps.v : &maps.k;
+    uint64_t* bar = hidden(i) ? &dirty[s] : &full[s];
+    if (!hidden(i)) mbar_arrive(&full[s]);
+    mbar_arrive_expect_tx(bar, L::kStage);
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c) tma_load_3d(st + c * 128 * 128, map, bar, c * 64, hk, ks + k_begin + (i >> 1) * kPromptKeys);
+  };
+  const int ahead = min(2 * n, L::kStages);
+  if (tid == 9 * 32) {  // the load warp: the first loads wait for nothing but the barriers
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(&full[s], 2);  // twice by the load warp, or once each by the two that clean the tile
       mbar_init(&empty[s], 1);
@@ -195,19 +198,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
     *abort_flag = 0;
     *spoiled = 0;
     fence_barrier_init();
+    for (int i = 0; i < ahead; ++i) load(i);
   }
+  __syncwarp();
   if (warp == 8) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  // the rows' queries, 16 bytes at a time; zeros behind the last row and column
-  for (int e = tid; e < kPromptRows * (DP / 8); e += kThreads) {
-    const int r = e / (DP / 8), c = e % (DP / 8), row = row0 + r;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < rows && 8 * c < p.dim)
-      v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + static_cast<long long>(qs + row / p.group) * p.q_row +
-                                          (hk * p.group + row % p.group) * p.q_head + 8 * c);
-    *reinterpret_cast<uint4*>(smem + (r / kTileRows) * L::kQTile + tile_at(r % kTileRows, c)) = v;
+  // The rows' queries, zeros behind the last row and column: a lane of the softmax
+  // warps finds its row's place, then a warp copies whole rows, all asked for at once.
+  constexpr int kLanes = DP / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows of a load
+  const int own_row = row0 + 32 * warp + lane;
+  if (warp < 8) {
+    const long long place = own_row < rows ? static_cast<long long>(qs + own_row / p.group) * p.q_row + (hk * p.group + own_row % p.group) * p.q_head : -1;
+    uint4 v[32 / kAtOnce];
+#pragma unroll
+    for (int i = 0; i < 32 / kAtOnce; ++i) {
+      const long long from = __shfl_sync(0xffffffffu, place, i * kAtOnce + lane / kLanes);
+      const int c = lane % kLanes;
+      v[i] = from >= 0 && 8 * c < p.dim ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + from + 8 * c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 32 / kAtOnce; ++i) {
+      const int r = 32 * warp + i * kAtOnce + lane / kLanes;
+      *reinterpret_cast<uint4*>(smem + (r / kTileRows) * L::kQTile + tile_at(r % kTileRows, lane % kLanes)) = v[i];
+    }
   }
   fence_proxy_async_smem();
   tc_fence_before();
@@ -220,19 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
     if (warp == 9) {
       // ------------------------------------------------------------ loads
       if (lane == 0) {
-        int i = 0;
-        auto hidden = [&](int i) { return (i & 1) && (i >> 1) >= first_hidden; };
-        for (; i < 2 * n; ++i) {  // K of key tile i / 2, then its V
-          const int s = i % L::kStages;
-          if (!mbar_wait(&empty[s], ((i / L::kStages) & 1) ^ 1, abort_flag, &g_status)) break;
-          uint8_t* st = smem + L::kRing + s * L::kStage;
-          const CUtensorMap* map = i & 1 ? &maps.v : &maps.k;
-          uint64_t* bar = hidden(i) ? &dirty[s] : &full[s];
-          if (!hidden(i)) mbar_arrive(&full[s]);
-          mbar_arrive_expect_tx(bar, L::kStage);
-#pragma unroll
-          for (int c = 0; c < DP / 64; ++c)
-            tma_load_3d(st + c * 128 * 128, map, bar, c * 64, hk, ks + k_begin + (i >> 1) * kPromptKeys);
+        int i = ahead;
+        for (; i < 2 * n; ++i) {
+          if (!mbar_wait(&empty[i % L::kStages], ((i / L::kStages) & 1) ^ 1, abort_flag, &g_status)) break;
+          load(i);
         }
         if (i < 2 * n) {  // gave up: the copies in flight land before the CTA ends
           volatile int no_abort = 0;
@@ -329,15 +335,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
         uint8_t* st = smem + L::kRing + stage * L::kStage;
         const int key0 = k_begin + j * kPromptKeys;
         bool any = false;
-        for (int e = (warp - 10) * 32 + lane; e < kPromptKeys * (DP / 8); e += 64) {
-          const int r = e / (DP / 8);
-          if (key0 + r <= first_limit) continue;
-          uint4* at16 = reinterpret_cast<uint4*>(st + tile_at(r, e % (DP / 8)));
-          uint4 v = *at16;
-          if (key0 + r >= kl)
-            *at16 = make_uint4(0, 0, 0, 0);
-          else if (drop_non_finite<T>(v))
-            *at16 = v, any = true;
+        constexpr int kPieces = kPromptKeys * (DP / 8) / 64;
+#pragma unroll 1
+        for (int i = 0; i < kPieces; i += 8) {
+          uint4 v[8];
+          uint4* at16[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int e = (warp - 10) * 32 + lane + 64 * (i + k);
+            at16[k] = reinterpret_cast<uint4*>(st + tile_at(e / (DP / 8), e % (DP / 8)));
+            v[k] = *at16[k];
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int key = key0 + ((warp - 10) * 32 + lane + 64 * (i + k)) / (DP / 8);
+            if (key <= first_limit) continue;
+            if (key >= kl)
+              *at16[k] = make_uint4(0, 0, 0, 0);
+            else if (drop_non_finite<T>(v[k]))
+              *at16[k] = v[k], any = true;
+          }
         }
         if (any) *spoiled = 1;
         fence_proxy_async_smem();
@@ -376,6 +393,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
           for (int e = 0; e < 32; ++e)
             if (32 * b + e > seen) s[b][e] = 0xFF800000u;  // minus infinity
       }
+      const float2 c2 = make_float2(c, c);
+      float2 base2, sum[4];  // a packed sum takes long: several chains of them
+      uint32_t pk[2][16];
+      // 64 of the scores to probabilities; where no key is hidden (those need 0
+      // exactly) two of eight pairs go by multiply-adds
+      auto half = [&](int h, auto mixed) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * h + b][2 * e]), __uint_as_float(s[2 * h + b][2 * e + 1])), c2, base2);
+            if (decltype(mixed)::value && (3 * e) % 8 < 2) {
+              x = exp2_pair(x);
+            } else {
+              x.x = exp2_fast(x.x);
+              x.y = exp2_fast(x.y);
+            }
+            sum[e % 4] = __fadd2_rn(sum[e % 4], x);
+            pk[b][e] = Half16<T>::pack(x.x, x.y);
+          }
+      };
+      auto hand_over = [&](int h) {
+        tmem_st16(scores + 32 * h, pk[0]);
+        tmem_st16(scores + 32 * h + 16, pk[1]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
+      };
       float top[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -390,52 +436,34 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
         if (grew) m = now;
         l *= factor;
         if (j > 0) {  // the last product is complete: these scores were issued after it
-#pragma unroll
-          for (int b = 0; b < DP; b += 32) {
-            uint32_t o[32];
-            tmem_ld32(result + b, o);
+#pragma unroll 1
+          for (int b = 0; b < DP; b += 16) {
+            uint32_t o[16];
+            tmem_ld16(result + b, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
-            tmem_st32(result + b, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+            tmem_st16(result + b, o);
           }
         }
       }
       const float base = (m == -INFINITY ? 0.f : m) * c;
-      const float2 c2 = make_float2(c, c), base2 = make_float2(-base, -base);
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      // MIXED: three of eight pairs by multiply-adds, where no key is hidden (those need 0 exactly)
-      auto half = [&](int h, auto mixed) {
+      base2 = make_float2(-base, -base);
 #pragma unroll
-        for (int b = 2 * h; b < 2 * h + 2; ++b) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 x = __ffma2_rn(make_float2(__uint_as_float(s[b][2 * e]), __uint_as_float(s[b][2 * e + 1])), c2, base2);
-            if (decltype(mixed)::value && (3 * e) % 8 < 3) {
-              x = exp2_pair(x);
-            } else {
-              x.x = exp2_fast(x.x);
-              x.y = exp2_fast(x.y);
-            }
-            sum[e & 1] = __fadd2_rn(sum[e & 1], x);
-            pk[e] = Half16<T>::pack(x.x, x.y);
-          }
-          tmem_st16(scores + 16 * b, pk);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
-      };
-      if (masked) {
+      for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
+      if (masked)
         half(0, std::false_type());
-        half(1, std::false_type());
-      } else {
+      else
         half(0, std::true_type());
+      hand_over(0);
+      if (masked)
+        half(1, std::false_type());
+      else
         half(1, std::true_type());
-      }
-      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      hand_over(1);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) sum[0] = __fadd2_rn(sum[0], sum[i]);
+      l += sum[0].x + sum[0].y;
     }
     if (nt > 0) {
       volatile int no_abort = 0;
@@ -450,7 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       const size_t slot = (static_cast<size_t>(share) * p.kv_heads + hk) * kPromptRows + row - row0;
       const bool write = row < rows && (!split || share < p.max_slots);
       const int spoil_end = *spoiled ? min(lim + 1, k_begin + nt * kStepN) : 0;
-      T* out = static_cast<T*>(p.out) + (static_cast<size_t>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim;
+      // a row's place in the output (or its slot), as the lanes that write it need it
+      const long long place = !write ? -1
+                              : split ? static_cast<long long>(slot) * DP
+                                      : (static_cast<long long>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim;
+      uint8_t* stage = smem + t * L::kQTile;  // the tile's queries are used up; each warp keeps to its rows
 #pragma unroll 1
       for (int b = 0; b < DP; b += 32) {
         uint32_t o[32];
@@ -461,31 +493,50 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        __syncwarp();  // the next load of tensor memory takes the whole warp
-        if (write) {
-          for (int key = max(k_begin, first_limit + 1); key < spoil_end; ++key) {
-            const T* v = static_cast<const T*>(p.v) + static_cast<long long>(ks + key) * p.v_row + hk * p.v_head + b;
+        for (int key = max(k_begin, first_limit + 1); key < spoil_end; ++key) {
+          const T* v = static_cast<const T*>(p.v) + static_cast<long long>(ks + key) * p.v_row + hk * p.v_head + b;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const uint32_t bits = b + e < p.dim ? reinterpret_cast<const uint16_t*>(v)[e] : 0u;
-              if ((bits & Half16<T>::kExp) == Half16<T>::kExp) o[e] = __float_as_uint(__uint_as_float(o[e]) + Half16<T>::to_float(bits));
-            }
-          }
-          if (split) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(p.part + slot * DP + b + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int h = 0; h < 4; ++h) w[h] = Half16<T>::pack(__uint_as_float(o[e + 2 * h]) * norm, __uint_as_float(o[e + 2 * h + 1]) * norm);
-              if (b + e < p.dim) *reinterpret_cast<uint4*>(out + b + e) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t bits = b + e < p.dim ? reinterpret_cast<const uint16_t*>(v)[e] : 0u;
+            if ((bits & Half16<T>::kExp) == Half16<T>::kExp) o[e] = __float_as_uint(__uint_as_float(o[e]) + Half16<T>::to_float(bits));
           }
         }
         __syncwarp();
+        if (split) {  // 32 float columns a row at a time: 128 bytes
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(stage + tile_at(32 * (warp & 3) + lane, e)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + lane / 8;
+            const long long to = __shfl_sync(0xffffffffu, place, r);
+            if (to >= 0)
+              *reinterpret_cast<uint4*>(p.part + to + b + 4 * (lane % 8)) = *reinterpret_cast<const uint4*>(stage + tile_at(32 * (warp & 3) + r, lane % 8));
+          }
+          __syncwarp();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) w[h] = Half16<T>::pack(__uint_as_float(o[e + 2 * h]) * norm, __uint_as_float(o[e + 2 * h + 1]) * norm);
+            *reinterpret_cast<uint4*>(stage + tile_at(32 * (warp & 3) + lane, (b + e) / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (!split) {
+        __syncwarp();
+        const int c = lane % kLanes;
+        uint4 v[32 / kAtOnce];
+#pragma unroll
+        for (int i = 0; i < 32 / kAtOnce; ++i)
+          v[i] = *reinterpret_cast<const uint4*>(stage + tile_at(32 * (warp & 3) + i * kAtOnce + lane / kLanes, c));
+#pragma unroll
+        for (int i = 0; i < 32 / kAtOnce; ++i) {
+          const long long to = __shfl_sync(0xffffffffu, place, i * kAtOnce + lane / kLanes);
+          if (to >= 0 && 8 * c < p.dim) *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to + 8 * c) = v[i];
+        }
       }
       if (split && write) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(m, l);
     }

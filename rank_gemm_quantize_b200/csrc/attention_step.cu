@@ -110,13 +110,13 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
 
   uint32_t used = 0;    // key tiles since the kernel's start
   uint32_t issued = 0;  // ... and how many of them thread 0 has asked for
-  Search at{0, 0, 0};
+  Search at{0, 0, 0, p.chunk};
   for (int item = CLUSTER ? blockIdx.x / kStepCluster : blockIdx.x;; item += gridDim.x) {
-    if (!find_item<kWarps>(p, at, item, &found, sums)) {  // a cluster's CTAs alike
+    Found f;
+    if (!find_item<kWarps>(p, at, item, &found, sums, &f)) {  // a cluster's CTAs alike
       if (CLUSTER) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
       return;
     }
-    const Found f = found;
     int qs, ql, ks, kl;
     seq_extent(p.q_offsets, f.b, p.q_rows, qs, ql);
     seq_extent(p.k_offsets, f.b, p.k_rows, ks, kl);
@@ -409,18 +409,21 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
   }
 }
 
-// Joins the shares: a row's softmax over all of them. CTA (b, key head, z)
-// takes rows z, z + gridDim.z, ..; its warps take every fourth share.
-template <class T, int DP>
+// Joins the shares: a row's softmax over all of them. CTA (b, key head, z) takes
+// WIDE rows at a time, z WIDE .., (z + gridDim.z) WIDE ..; 4 / WIDE warps divide a
+// row's shares among them (WIDE 1: few rows of many shares; 4: many of few).
+template <class T, int DP, int WIDE>
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnParams p) {
+  constexpr int kSplit = kWarps / WIDE;
   __shared__ int sums[kWarps];
   __shared__ float warp_ml[kWarps][2];
   __shared__ float warp_o[kWarps][DP];
   const int b = blockIdx.x, hk = blockIdx.y, warp = warp_id(), lane = lane_id();
-  const Shares s = shares_of(p, b);
+  const int chunk = key_chunk(p);
+  const Shares s = shares_of(p, b, chunk);
   if (!s.slots) return;
   int before = 0;
-  for (int j = threadIdx.x; j < b; j += kThreads) before += shares_of(p, j).slots;
+  for (int j = threadIdx.x; j < b; j += kThreads) before += shares_of(p, j, chunk).slots;
   before = __shfl_sync(0xffffffffu, warp_inclusive(before), 31);
   if (lane == 0) sums[warp] = before;
   __syncthreads();
@@ -429,13 +432,15 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnPara
   int qs, ql;
   seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
   constexpr int kPer = DP / 32;
-  for (int row = blockIdx.z; row < ql * p.group; row += gridDim.z) {
+  const int rows = ql * p.group;
+  for (int row0 = blockIdx.z * WIDE; row0 < rows; row0 += gridDim.z * WIDE) {
+    const int row = min(row0 + warp / kSplit, rows - 1);
     const int first = before + row / p.tile_rows * s.chunks, r = row % p.tile_rows;
     float top = -INFINITY, total = 0.f, o[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[e] = 0.f;
 #pragma unroll 4
-    for (int c = warp; c < s.chunks; c += kWarps) {
+    for (int c = warp % kSplit; c < s.chunks; c += kSplit) {
       const size_t slot = (static_cast<size_t>(first + c) * p.kv_heads + hk) * p.tile_rows + r;
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot);
       float v[kPer];
@@ -448,35 +453,41 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnPara
 #pragma unroll
       for (int e = 0; e < kPer; ++e) o[e] = fmaf(o[e], was, v[e] * w);
     }
-    if (lane == 0) {
-      warp_ml[warp][0] = top;
-      warp_ml[warp][1] = total;
-    }
+    if constexpr (kSplit > 1) {
+      if (lane == 0) {
+        warp_ml[warp][0] = top;
+        warp_ml[warp][1] = total;
+      }
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) warp_o[warp][kPer * lane + e] = o[e];
-    __syncthreads();
-    if (threadIdx.x < DP / 2) {
-      const int c = 2 * threadIdx.x;
+      for (int e = 0; e < kPer; ++e) warp_o[warp][kPer * lane + e] = o[e];
+      __syncthreads();
       top = -INFINITY;
 #pragma unroll
-      for (int a = 0; a < kWarps; ++a) top = fmaxf(top, warp_ml[a][0]);
+      for (int a = 0; a < kSplit; ++a) top = fmaxf(top, warp_ml[a][0]);
       const float base = (top == -INFINITY ? 0.f : top) * p.scale_log2;
-      float x = 0.f, y = 0.f;
       total = 0.f;
 #pragma unroll
-      for (int a = 0; a < kWarps; ++a) {
+      for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+#pragma unroll
+      for (int a = 0; a < kSplit; ++a) {
         const float w = exp2_fast(fmaf(warp_ml[a][0], p.scale_log2, -base));
         total = fmaf(warp_ml[a][1], w, total);
-        x = fmaf(warp_o[a][c], w, x);
-        y = fmaf(warp_o[a][c + 1], w, y);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] = fmaf(warp_o[a][kPer * lane + e], w, o[e]);
       }
-      const float norm = total == 0.f ? 1.f : 1.f / total;
-      if (c < p.dim)
-        *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) +
-                                     (static_cast<size_t>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim + c) =
-            Half16<T>::pack(x * norm, y * norm);
+      __syncthreads();
+      if (warp > 0) continue;
+    } else if (row0 + warp >= rows) {
+      continue;
     }
-    __syncthreads();
+    const float norm = total == 0.f ? 1.f : 1.f / total;
+    if (kPer * lane < p.dim) {
+      T* out = static_cast<T*>(p.out) + (static_cast<size_t>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim + kPer * lane;
+      if constexpr (kPer == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(Half16<T>::pack(o[0] * norm, o[1] * norm), Half16<T>::pack(o[2] * norm, o[3] * norm));
+      else
+        *reinterpret_cast<uint32_t*>(out) = Half16<T>::pack(o[0] * norm, o[1] * norm);
+    }
   }
 }
 
@@ -511,7 +522,13 @@ cudaError_t start(const AttnParams& p, const AttnMaps& maps, int sms, cudaStream
 template <class T, int DP>
 cudaError_t join(const AttnParams& p, cudaStream_t st) {
   const long long rows = (static_cast<long long>(p.q_rows) * p.group + p.batch - 1) / p.batch;
-  attention_join_kernel<T, DP><<<dim3(p.batch, p.kv_heads, static_cast<int>(std::min<long long>(rows, 4096))), kThreads, 0, st>>>(p);
+  const bool wide = p.tile_rows > kStepRows;
+  const int z = static_cast<int>(std::min<long long>(wide ? (rows + 3) / 4 : rows, 4096));
+  const dim3 grid(p.batch, p.kv_heads, z);
+  if (wide)
+    attention_join_kernel<T, DP, 4><<<grid, kThreads, 0, st>>>(p);
+  else
+    attention_join_kernel<T, DP, 1><<<grid, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
