@@ -206,6 +206,68 @@ def test_many_sequences():
     check(18, q_lengths, k_lengths, 2, 1, 64, BF16, True)
 
 
+def test_many_prompts():
+    """More sequences than lanes of a warp, through the kernel for many queries."""
+    g = torch.Generator().manual_seed(22)
+    lengths = torch.randint(30, 200, (45,), generator=g).tolist()
+    lengths[7] = 0
+    check(23, lengths, [n + 3 for n in lengths], 4, 2, 64, BF16, True)
+
+
+def test_scores_that_keep_growing():
+    """Keys in the order of their scores: the running maximum grows all along, far past any threshold."""
+    for n, m, dtype in ((1, 3000, F16), (200, 1500, BF16), (150, 1200, F16)):
+        q, k, v = make(24, [n], [m], 2, 1, 64, dtype)
+        direction = torch.zeros(64)
+        direction[0] = 1
+        k[:, 0] = (torch.linspace(-20, 20, m)[:, None] * direction).to(dtype).cuda() + 0.1 * k[:, 0]
+        q[:] = (30 * direction).to(dtype).cuda()
+        for causal in (False, True):
+            ops.check(run(q, k, v, [n], [m], causal), *ops.attention(q, k, v, [n], [m], causal))
+
+
+@pytest.mark.parametrize("q_lengths,k_lengths", [([1, 1], [900, 30]), ([1, 1], [30000, 500]), ([200], [200]), ([300, 20], [5000, 900])])
+def test_two_calls_at_once(q_lengths, k_lengths):
+    """The same call on two streams, with workspaces of their own."""
+    import rank_gemm_quantize_b200 as rq
+    inputs = [make(s, q_lengths, k_lengths, 4, 2, 128, BF16) for s in (25, 26)]
+    qo, ko = offsets(q_lengths), offsets(k_lengths)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [rq.attention(q, k, v, qo, ko, causal=True, stream=s) for (q, k, v), s in zip(inputs, streams)]
+    torch.cuda.synchronize()
+    for o, (q, k, v) in zip(got, inputs):
+        ops.check(o, *ops.attention(q, k, v, q_lengths, k_lengths, True))
+
+
+def test_keys_and_queries_of_one_tensor_and_one_row():
+    """q, k and v the same tensor; a single row whose strides mean nothing."""
+    import rank_gemm_quantize_b200 as rq
+    q, _, _ = make(27, [90], [90], 2, 2, 64, BF16)
+    ops.check(rq.attention(q, q, q, causal=True), *ops.attention(q, q, q, [90], [90], True))
+    row = torch.randn(3, 2, 64).to(BF16).cuda().as_strided((1, 2, 64), (7, 64, 1))
+    ops.check(rq.attention(row, row, row), *ops.attention(row, row, row, [1], [1], False))
+
+
+def test_refused_views():
+    import rank_gemm_quantize_b200 as rq
+    q, k, v = make(28, [8], [8], 2, 2, 64, BF16)
+    with pytest.raises(ValueError, match="contiguous"):
+        rq.attention(q.transpose(1, 2).contiguous().transpose(1, 2), k, v)
+    with pytest.raises(rq.SvdqError, match="strides"):
+        rq.attention(q, k[:1].expand(8, 2, 64), v)
+    with pytest.raises(rq.SvdqError, match="aligned"):
+        flat = torch.zeros(8 * 128 + 4, dtype=BF16, device="cuda")
+        rq.attention(flat[4:].view(8, 2, 64), k, v)
+    with pytest.raises(ValueError, match="k_offsets"):
+        rq.attention(q[:3], k, v, offsets([3]))
+    with pytest.raises(ValueError, match="int32"):
+        rq.attention(q, k, v, offsets([8]).long())
+    with pytest.raises(ValueError, match="all float16"):
+        rq.attention(q, k, v.half())
+
+
 def test_nothing_to_do():
     import rank_gemm_quantize_b200 as rq
     q, k, v = make(19, [0], [5], 4, 2, 64, BF16)

@@ -69,6 +69,26 @@ def test_larger(M, K, N):
     check(5, M, K, N, BF16, "silu")
 
 
+@pytest.mark.parametrize("M,K,N", [(9000, 64, 8), (8500, 8, 72), (300, 40, 8200), (257, 1000, 8192), (4097, 520, 1000)])
+def test_many_tiles(M, K, N):
+    """Two SMs a tile: one column block or row block, a ragged last one, little to sum."""
+    check(11, M, K, N, BF16, "gelu_tanh")
+    check(12, M, K, N, F16, None, bias=False)
+
+
+def test_two_calls_at_once():
+    """On two streams, large and small, each right."""
+    import rank_gemm_quantize_b200 as rq
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    cases = [make(13, 2000, 1024, 1032, BF16), make(14, 3, 4096, 2048, BF16)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [rq.linear(X, W, b, "relu", r, stream=s) for (X, W, b, r), s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for y, (X, W, b, r) in zip(got, cases):
+        ops.check(y, *ops.linear(X, W, b, "relu", r))
+
+
 def test_in_place_on_the_residual():
     import rank_gemm_quantize_b200 as rq
     for M in (4, 150, 1200):
