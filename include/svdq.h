@@ -367,23 +367,21 @@ typedef struct {
   long long q_row_stride, q_head_stride;
   long long k_row_stride, k_head_stride;
   long long v_row_stride, v_head_stride;
-} svdq_attention_config;
+  const void* q;           /* device [q_rows, q_heads, head_dim], strided as above */
+  const void *k, *v;       /* device [k_rows, kv_heads, head_dim], strided as above */
+  const int *q_offsets, *k_offsets; /* device int32 [batch + 1]; NULL only for batch 1 (all rows) */
+  void* out;               /* device [q_rows, q_heads, head_dim]; overlaps no input. Rows of no sequence are left as they are. */
+  void* workspace;         /* svdq_attention_workspace_size bytes or more, 256-byte aligned, not initialised; NULL where that is 0 */
+  unsigned long long workspace_bytes;
+} svdq_attention_args;
 
-/* Bytes of workspace svdq_attention_forward needs (it depends on the device's
- * SM count: query it on the device of the call; 0 is possible). */
-SVDQ_API svdq_status svdq_attention_workspace_size(const svdq_attention_config* cfg, size_t* bytes);
-/*   q          device [q_rows, q_heads, head_dim] with cfg's strides
- *   k, v       device [k_rows, kv_heads, head_dim] with cfg's strides
- *   q_offsets, k_offsets  device int32 [batch + 1]; NULL only for batch 1 (all rows)
- *   out        device [q_rows, q_heads, head_dim]; overlaps no input. Rows that
- *              belong to no sequence are left as they are.
- *   workspace  at least svdq_attention_workspace_size bytes, 256-byte aligned,
- *              no initialisation needed (may be NULL when the size is 0).
- * q, k, v and out 16-byte aligned. One kernel on `stream`, or two where the
- * keys of few queries are split over the SMs and joined. */
-SVDQ_API svdq_status svdq_attention_forward(const svdq_attention_config* cfg, const void* q, const void* k,
-                                            const void* v, const int* q_offsets, const int* k_offsets, void* out,
-                                            void* workspace, size_t workspace_bytes, void* stream);
+/* Bytes of workspace svdq_attention_forward needs: it goes by dtype, batch,
+ * rows, heads and head_dim, and by the current device's SM count (the
+ * addresses are not looked at). 0 is possible. */
+SVDQ_API svdq_status svdq_attention_workspace_size(const svdq_attention_args* args, size_t* bytes);
+/* q, k, v and out 16-byte aligned. One kernel on `stream`, or two where the
+ * keys are split over the SMs and joined through the workspace. */
+SVDQ_API svdq_status svdq_attention_forward(const svdq_attention_args* args, void* stream);
 
 typedef enum {
   SVDQ_ACT_NONE = 0,
@@ -395,16 +393,20 @@ typedef enum {
 
 /* A linear layer whose weight stays in 16 bits, read in place:
  *     Y = residual + act(X W + bias)
- * with float accumulation, and one rounding at the end.
- *   dtype     SVDQ_BF16 or SVDQ_F16, of every tensor
- *   X         device [M, K];  W device [K, N];  K and N multiples of 8
- *   bias      device [N] or NULL
- *   residual  device [M, N] or NULL
- *   Y         device [M, N]; may be the residual itself, overlaps nothing else
- * All 16-byte aligned. M = 0 is allowed (nothing happens). One kernel on `stream`. */
-SVDQ_API svdq_status svdq_dense_linear_forward(int dtype, const void* X, const void* W, const void* bias,
-                                               const void* residual, int activation, int M, int K, int N, void* Y,
-                                               void* stream);
+ * with float accumulation, and one rounding at the end. */
+typedef struct {
+  int dtype;               /* SVDQ_BF16 or SVDQ_F16, of every tensor */
+  int activation;          /* svdq_activation */
+  int M, K, N;             /* K and N multiples of 8; M = 0: nothing happens */
+  const void* X;           /* device [M, K] */
+  const void* W;           /* device [K, N] */
+  const void* bias;        /* device [N] or NULL */
+  const void* residual;    /* device [M, N] or NULL */
+  void* Y;                 /* device [M, N]; may be the residual itself, overlaps nothing else */
+} svdq_dense_linear_args;
+
+/* All tensors contiguous and 16-byte aligned. One kernel on `stream`. */
+SVDQ_API svdq_status svdq_dense_linear_forward(const svdq_dense_linear_args* args, void* stream);
 
 typedef enum {
   SVDQ_NORM_NONE = 0,

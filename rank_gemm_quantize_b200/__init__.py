@@ -73,7 +73,14 @@ class _Attention(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int), ("batch", ctypes.c_int), ("q_rows", ctypes.c_int), ("k_rows", ctypes.c_int),
                 ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
                 ("causal", ctypes.c_int), ("scale", ctypes.c_float)] + [
-                    (f"{t}_{a}_stride", ctypes.c_longlong) for t in "qkv" for a in ("row", "head")]
+                    (f"{t}_{a}_stride", ctypes.c_longlong) for t in "qkv" for a in ("row", "head")] + [
+                        (n, ctypes.c_void_p) for n in ("q", "k", "v", "q_offsets", "k_offsets", "out", "workspace")] + [
+                            ("workspace_bytes", ctypes.c_ulonglong)]
+
+
+class _DenseLinear(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "activation", "M", "K", "N")] + [
+        (n, ctypes.c_void_p) for n in ("X", "W", "bias", "residual", "Y")]
 
 
 class _ResidualNorm(ctypes.Structure):
@@ -85,11 +92,11 @@ class _ResidualNorm(ctypes.Structure):
 
 def _packer(cls):
     """Packs a call's arguments as the C struct, without the cost of a ctypes object (0 for NULL)."""
-    code = {ctypes.c_int: "i", ctypes.c_float: "f", ctypes.c_void_p: "P", ctypes.c_longlong: "q"}
+    code = {ctypes.c_int: "i", ctypes.c_float: "f", ctypes.c_void_p: "P", ctypes.c_longlong: "q", ctypes.c_ulonglong: "Q"}
     return struct.Struct("@" + "".join(code[t] for _, t in cls._fields_)).pack
 
 
-_pack_attention, _pack_residual_norm = _packer(_Attention), _packer(_ResidualNorm)
+_pack_attention, _pack_dense_linear, _pack_residual_norm = map(_packer, (_Attention, _DenseLinear, _ResidualNorm))
 
 # Every symbol include/svdq.h declares, with its ctypes signature.
 _VP, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -121,8 +128,8 @@ SIGNATURES = {
     "svdq_w4a16_export": [_VP, _VP, _VP, _VP],
     "svdq_w4a16_destroy": [_VP],
     "svdq_attention_workspace_size": [_VP, ctypes.POINTER(_SZ)],
-    "svdq_attention_forward": [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP],
-    "svdq_dense_linear_forward": [_I, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP],
+    "svdq_attention_forward": [_VP, _VP],
+    "svdq_dense_linear_forward": [_VP, _VP],
     "svdq_residual_norm": [_VP, _VP],
     "svdq_operator_status": [_VP],
 }
@@ -543,7 +550,7 @@ def _attention_need(device: int, *shapes: int) -> int:
     heads, kv_heads, dim = shapes[4:]
     n = ctypes.c_size_t()
     _check(lib().svdq_attention_workspace_size(
-        _pack_attention(*shapes, 0, 1.0, heads * dim, dim, kv_heads * dim, dim, kv_heads * dim, dim), ctypes.byref(n)))
+        _pack_attention(*shapes, 0, 1.0, heads * dim, dim, kv_heads * dim, dim, kv_heads * dim, dim, *[0] * 8), ctypes.byref(n)))
     return n.value
 
 
@@ -572,11 +579,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opti
     if device != _current_device():
         with torch.cuda.device(device):
             return attention(q, k, v, q_offsets, k_offsets, causal, scale, out, workspace, stream)
-    if q_offsets is None:
-        if k_offsets is not None:
-            raise ValueError("k_offsets need q_offsets")
-        batch, qo, ko = 1, None, None
-    else:
+    batch, qo, ko = 1, 0, 0
+    if q_offsets is not None:
         qo, batch = _offsets("q_offsets", q_offsets, device), q_offsets.shape[0] - 1
         if k_offsets is None:
             if q.shape[0] != k.shape[0]:
@@ -586,24 +590,29 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opti
             ko = _offsets("k_offsets", k_offsets, device)
             if k_offsets.shape[0] != batch + 1:
                 raise ValueError("q_offsets and k_offsets must be of the same length")
+    elif k_offsets is not None:
+        raise ValueError("k_offsets need q_offsets")
     shapes = _attention_shapes(q, k, v, batch)
     (qr, qh, q1), (kr, kh, k1), (vr, vh, v1) = q.stride(), k.stride(), v.stride()
     if q1 != 1 or k1 != 1 or v1 != 1:
         raise ValueError("the values of a head of q, k and v must be contiguous")
-    cfg = _pack_attention(*shapes, 1 if causal else 0, shapes[6] ** -0.5 if scale is None else scale, qr, qh, kr, kh, vr, vh)
-    need = _attention_need(device, *shapes)
     made_out = made_workspace = None
     if out is None:
         out = made_out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(tuple(q.shape))
-    o = _operand("out", out, q.dtype, device, q.shape)
-    if workspace is None:
-        if need:
-            workspace = made_workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != device:
-        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    _check(lib().svdq_attention_forward(cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), qo, ko, o, ws, size,
-                                        _call_stream(device, stream, made_out, made_workspace)))
+        o = out.data_ptr()
+    else:
+        o = _operand("out", out, q.dtype, device, q.shape)
+    ws, need = 0, _attention_need(device, *shapes)
+    if workspace is not None:
+        if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != device:
+            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+        ws, need = workspace.data_ptr(), workspace.numel()
+    elif need:
+        made_workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = made_workspace.data_ptr()
+    args = _pack_attention(*shapes, 1 if causal else 0, shapes[6] ** -0.5 if scale is None else scale, qr, qh, kr, kh, vr, vh,
+                           q.data_ptr(), k.data_ptr(), v.data_ptr(), qo, ko, o, ws, need)
+    _check(lib().svdq_attention_forward(args, _call_stream(device, stream, made_out, made_workspace)))
     return out
 
 
@@ -624,15 +633,19 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
         with torch.cuda.device(device):
             return linear(X, W, bias, activation, residual, out, stream)
     (M, K), N = X.shape, W.shape[1]
-    x = _operand("X", X, dtype, device, (M, K))
+    if not X.is_contiguous():
+        raise ValueError("X must be contiguous")
     w = _operand("W", W, dtype, device, (K, N))
-    b = None if bias is None else _operand("bias", bias, dtype, device, (N,))
-    r = None if residual is None else _operand("residual", residual, dtype, device, (M, N))
+    b = 0 if bias is None else _operand("bias", bias, dtype, device, (N,))
+    r = 0 if residual is None else _operand("residual", residual, dtype, device, (M, N))
     made = None
     if out is None:
         out = made = X.new_empty((M, N))
-    y = _operand("out", out, dtype, device, (M, N))
-    _check(lib().svdq_dense_linear_forward(_DTYPE[dtype], x, w, b, r, act, M, K, N, y, _call_stream(device, stream, made)))
+        y = out.data_ptr()
+    else:
+        y = _operand("out", out, dtype, device, (M, N))
+    args = _pack_dense_linear(_DTYPE[dtype], act, M, K, N, X.data_ptr(), w, b, r, y)
+    _check(lib().svdq_dense_linear_forward(args, _call_stream(device, stream, made)))
     return out
 
 
@@ -671,6 +684,8 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
             return residual_norm(x, y, offsets=offsets, gate=gate, residual_scale=residual_scale, post_norm=post_norm,
                                  post_weight=post_weight, post_bias=post_bias, norm=norm, weight=weight, bias=bias,
                                  scale=scale, shift=shift, eps=eps, dtype=dtype, out_x=out_x, out_h=out_h, stream=stream)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     shape = x.shape
     rows, dim = shape
     x_kind = x.dtype
@@ -682,19 +697,23 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
         gate, scale, shift = (None if t is None else t.view(1, -1) if t.dim() == 1 else t for t in (gate, scale, shift))
     if y is not None:
         if out_x is None:
-            out_x = made_x = torch.empty_like(x, memory_format=torch.contiguous_format)
-        x_out = _operand("out_x", out_x, x_kind, device, shape)
+            out_x = made_x = torch.empty_like(x)
+            x_out = out_x.data_ptr()
+        else:
+            x_out = _operand("out_x", out_x, x_kind, device, shape)
     elif out_x is not None:
         raise ValueError("without y there is no out_x")
     if norm is not None:
         if out_h is None:
-            out_h = made_h = torch.empty_like(x if y is None else y, dtype=kind, memory_format=torch.contiguous_format)
-        h_out = _operand("out_h", out_h, kind, device, shape)
+            out_h = made_h = torch.empty_like(x, dtype=kind)
+            h_out = out_h.data_ptr()
+        else:
+            h_out = _operand("out_h", out_h, kind, device, shape)
     elif out_h is not None:
         raise ValueError("without a norm there is no out_h")
     args = _pack_residual_norm(
         _DTYPE[kind], _DTYPE[x_kind], rows, dim, seqs, _NORM[post_norm], _NORM[norm], residual_scale, eps,
-        _operand("x", x, x_kind, device, shape), 0 if y is None else _operand("y", y, kind, device, shape), x_out, h_out,
+        x.data_ptr(), 0 if y is None else _operand("y", y, kind, device, shape), x_out, h_out,
         0 if gate is None else _operand("gate", gate, kind, device, of_seq),
         0 if post_weight is None else _operand("post_weight", post_weight, kind, device, of_row),
         0 if post_bias is None else _operand("post_bias", post_bias, kind, device, of_row),

@@ -23,8 +23,8 @@ svdq_status fail(svdq_status st, const std::string& msg) {
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
-svdq_status check(const svdq_attention_config* c) {
-  if (!c) return fail(SVDQ_ERR_INVALID_ARG, "cfg is NULL");
+svdq_status check(const svdq_attention_args* c) {
+  if (!c) return fail(SVDQ_ERR_INVALID_ARG, "args is NULL");
   if (c->dtype != SVDQ_BF16 && c->dtype != SVDQ_F16) return fail(SVDQ_ERR_INVALID_ARG, "unknown dtype");
   if (c->batch < 1 || c->q_rows < 0 || c->k_rows < 0) return fail(SVDQ_ERR_INVALID_ARG, "bad batch, q_rows or k_rows");
   if (c->batch > 65535) return fail(SVDQ_ERR_UNSUPPORTED, "batch exceeds 65535");
@@ -58,7 +58,7 @@ struct Plan {
 // Which kernel, and the shares the keys are cut into. The lengths of the
 // sequences are on the device: the rules go by the totals, and both kernels are
 // right for any lengths.
-svdq_status plan(const svdq_attention_config* c, Plan* out) {
+svdq_status plan(const svdq_attention_args* c, Plan* out) {
   int dev = 0;
   Plan p{};
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&p.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -102,7 +102,7 @@ svdq_status plan(const svdq_attention_config* c, Plan* out) {
   return SVDQ_OK;
 }
 
-bool make_kv_map(CUtensorMap* m, const svdq_attention_config* c, const void* base, long long row, long long head, int keys) {
+bool make_kv_map(CUtensorMap* m, const svdq_attention_args* c, const void* base, long long row, long long head, int keys) {
   const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim), static_cast<uint64_t>(c->kv_heads), static_cast<uint64_t>(c->k_rows)};
   // a single head or row has no stride of its own: any legal one
   const uint64_t strides[2] = {static_cast<uint64_t>(c->kv_heads > 1 ? head : c->head_dim) * 2,
@@ -116,61 +116,59 @@ bool make_kv_map(CUtensorMap* m, const svdq_attention_config* c, const void* bas
 
 extern "C" {
 
-svdq_status svdq_attention_workspace_size(const svdq_attention_config* cfg, size_t* bytes) {
-  if (svdq_status e = check(cfg)) return e;
+svdq_status svdq_attention_workspace_size(const svdq_attention_args* args, size_t* bytes) {
+  if (svdq_status e = check(args)) return e;
   if (!bytes) return fail(SVDQ_ERR_INVALID_ARG, "bytes is NULL");
   Plan p;
-  if (svdq_status e = plan(cfg, &p)) return e;
+  if (svdq_status e = plan(args, &p)) return e;
   *bytes = p.total;
   return SVDQ_OK;
 }
 
-svdq_status svdq_attention_forward(const svdq_attention_config* cfg, const void* q, const void* k, const void* v,
-                                   const int* q_offsets, const int* k_offsets, void* out, void* workspace,
-                                   size_t workspace_bytes, void* stream) {
-  if (svdq_status e = check(cfg)) return e;
-  if (cfg->q_rows == 0) return SVDQ_OK;
-  if (!q || !out || (cfg->k_rows > 0 && (!k || !v))) return fail(SVDQ_ERR_INVALID_ARG, "q, k, v or out is NULL");
-  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
+svdq_status svdq_attention_forward(const svdq_attention_args* a, void* stream) {
+  if (svdq_status e = check(a)) return e;
+  if (a->q_rows == 0) return SVDQ_OK;
+  if (!a->q || !a->out || (a->k_rows > 0 && (!a->k || !a->v))) return fail(SVDQ_ERR_INVALID_ARG, "q, k, v or out is NULL");
+  if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->out, 16))
     return fail(SVDQ_ERR_INVALID_ARG, "q, k, v and out must be 16-byte aligned");
-  if ((!q_offsets || !k_offsets) && cfg->batch != 1) return fail(SVDQ_ERR_INVALID_ARG, "several sequences need offsets");
-  if (!aligned(q_offsets, 4) || !aligned(k_offsets, 4)) return fail(SVDQ_ERR_INVALID_ARG, "offsets must be 4-byte aligned");
+  if ((!a->q_offsets || !a->k_offsets) && a->batch != 1) return fail(SVDQ_ERR_INVALID_ARG, "several sequences need offsets");
+  if (!aligned(a->q_offsets, 4) || !aligned(a->k_offsets, 4)) return fail(SVDQ_ERR_INVALID_ARG, "offsets must be 4-byte aligned");
   Plan pl;
-  if (svdq_status e = plan(cfg, &pl)) return e;
-  if (pl.total && (!workspace || !aligned(workspace, 256) || workspace_bytes < pl.total))
+  if (svdq_status e = plan(a, &pl)) return e;
+  if (pl.total && (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < pl.total))
     return fail(SVDQ_ERR_INVALID_ARG, "workspace missing, misaligned or too small");
   AttnParams p{};
-  p.q = q;
-  p.v = v;
-  p.out = out;
-  p.q_offsets = q_offsets;
-  p.k_offsets = k_offsets;
-  p.batch = cfg->batch;
-  p.q_rows = cfg->q_rows;
-  p.k_rows = cfg->k_rows;
-  p.q_heads = cfg->q_heads;
-  p.kv_heads = cfg->kv_heads;
-  p.group = cfg->q_heads / cfg->kv_heads;
-  p.dim = cfg->head_dim;
-  p.causal = cfg->causal;
-  p.scale_log2 = cfg->scale * 1.4426950408889634f;
-  p.q_row = cfg->q_row_stride;
-  p.q_head = cfg->q_head_stride;
-  p.v_row = cfg->v_row_stride;
-  p.v_head = cfg->v_head_stride;
+  p.q = a->q;
+  p.v = a->v;
+  p.out = a->out;
+  p.q_offsets = a->q_offsets;
+  p.k_offsets = a->k_offsets;
+  p.batch = a->batch;
+  p.q_rows = a->q_rows;
+  p.k_rows = a->k_rows;
+  p.q_heads = a->q_heads;
+  p.kv_heads = a->kv_heads;
+  p.group = a->q_heads / a->kv_heads;
+  p.dim = a->head_dim;
+  p.causal = a->causal;
+  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.q_row = a->q_row_stride;
+  p.q_head = a->q_head_stride;
+  p.v_row = a->v_row_stride;
+  p.v_head = a->v_head_stride;
   p.tile_rows = pl.prompt ? kPromptRows : kStepRows;
   p.split_tiles = pl.prompt ? INT_MAX : kStepSplitTiles;
   p.chunk = pl.open ? 0 : pl.chunk;
   p.fill = pl.fill;
   p.max_slots = pl.max_slots;
-  p.part = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.ml);
+  p.part = static_cast<float*>(a->workspace);
+  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + pl.ml);
   AttnMaps maps{};
   const int key_tile = pl.prompt ? kPromptKeys : kStepKeys;
-  if (cfg->k_rows > 0 && (!make_kv_map(&maps.k, cfg, k, cfg->k_row_stride, cfg->k_head_stride, key_tile) ||
-                          !make_kv_map(&maps.v, cfg, v, cfg->v_row_stride, cfg->v_head_stride, key_tile)))
+  if (a->k_rows > 0 && (!make_kv_map(&maps.k, a, a->k, a->k_row_stride, a->k_head_stride, key_tile) ||
+                          !make_kv_map(&maps.v, a, a->v, a->v_row_stride, a->v_head_stride, key_tile)))
     return fail(SVDQ_ERR_CUDA, "cuTensorMapEncodeTiled (keys or values) failed");
-  const bool bf16 = cfg->dtype == SVDQ_BF16;
+  const bool bf16 = a->dtype == SVDQ_BF16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = pl.prompt ? launch_attention_prompt(p, maps, bf16, st) : launch_attention_step(p, maps, bf16, pl.cluster, pl.sms, st);
   if (e == cudaSuccess && pl.max_slots > 0) e = launch_attention_join(p, bf16, st);

@@ -580,19 +580,19 @@ namespace svdq {
 cudaError_t take_status_dense(int* status, cudaStream_t st) { return take_status(status, st); }
 }  // namespace svdq
 
-extern "C" svdq_status svdq_dense_linear_forward(int dtype, const void* X, const void* W, const void* bias, const void* residual,
-                                                 int activation, int M, int K, int N, void* Y, void* stream) {
-  if (dtype != SVDQ_BF16 && dtype != SVDQ_F16) return fail(SVDQ_ERR_INVALID_ARG, "unknown dtype");
-  if (activation < SVDQ_ACT_NONE || activation > SVDQ_ACT_GELU_TANH) return fail(SVDQ_ERR_INVALID_ARG, "unknown activation");
-  if (M < 0 || K <= 0 || N <= 0 || K % 8 || N % 8)
+extern "C" svdq_status svdq_dense_linear_forward(const svdq_dense_linear_args* a, void* stream) {
+  if (!a) return fail(SVDQ_ERR_INVALID_ARG, "args is NULL");
+  if (a->dtype != SVDQ_BF16 && a->dtype != SVDQ_F16) return fail(SVDQ_ERR_INVALID_ARG, "unknown dtype");
+  if (a->activation < SVDQ_ACT_NONE || a->activation > SVDQ_ACT_GELU_TANH) return fail(SVDQ_ERR_INVALID_ARG, "unknown activation");
+  if (a->M < 0 || a->K <= 0 || a->N <= 0 || a->K % 8 || a->N % 8)
     return fail(SVDQ_ERR_INVALID_ARG, "M must not be negative, K and N positive multiples of 8");
-  if (M > 1 << 22 || K > 1 << 22 || N > 1 << 22) return fail(SVDQ_ERR_UNSUPPORTED, "M, K or N exceeds 4194304");
-  if (M == 0) return SVDQ_OK;
-  if (!X || !W || !Y) return fail(SVDQ_ERR_INVALID_ARG, "X, W or Y is NULL");
+  if (a->M > 1 << 22 || a->K > 1 << 22 || a->N > 1 << 22) return fail(SVDQ_ERR_UNSUPPORTED, "M, K or N exceeds 4194304");
+  if (a->M == 0) return SVDQ_OK;
+  if (!a->X || !a->W || !a->Y) return fail(SVDQ_ERR_INVALID_ARG, "X, W or Y is NULL");
   uintptr_t bits = 0;
-  for (const void* q : {X, W, bias, residual, static_cast<const void*>(Y)}) bits |= reinterpret_cast<uintptr_t>(q);
+  for (const void* q : {a->X, a->W, a->bias, a->residual, static_cast<const void*>(a->Y)}) bits |= reinterpret_cast<uintptr_t>(q);
   if (bits & 15) return fail(SVDQ_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
-  const DenseParams p{bias, residual, Y, M, N, K, activation};
+  const DenseParams p{a->bias, a->residual, a->Y, a->M, a->N, a->K, a->activation};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == SVDQ_BF16 ? run<__nv_bfloat16>(p, X, W, st) : run<__half>(p, X, W, st);
+  return a->dtype == SVDQ_BF16 ? run<__nv_bfloat16>(p, a->X, a->W, st) : run<__half>(p, a->X, a->W, st);
 }

@@ -23,10 +23,11 @@ def refused(rq, status, want, message):
     assert message in rq.lib().svdq_last_error()
 
 
-def attention_config(rq, **change):
+def attention_args(rq, **change):
     c = rq._Attention(dtype=0, batch=1, q_rows=4, k_rows=9, q_heads=4, kv_heads=2, head_dim=64, causal=1, scale=0.125,
                       q_row_stride=256, q_head_stride=64, k_row_stride=128, k_head_stride=64, v_row_stride=128,
-                      v_head_stride=64)
+                      v_head_stride=64, q=FAKE, k=FAKE, v=FAKE, q_offsets=FAKE, k_offsets=FAKE, out=FAKE, workspace=FAKE,
+                      workspace_bytes=1 << 30)
     for name, value in change.items():
         setattr(c, name, value)
     return c
@@ -44,10 +45,9 @@ def attention_config(rq, **change):
     (dict(v_head_stride=-64), INVALID, b"strides"), (dict(k_head_stride=1 << 38), INVALID, b"strides"),
 ])
 def test_attention_refuses_bad_configurations(rq, change, status, message):
-    c, n = attention_config(rq, **change), ctypes.c_size_t()
+    c, n = attention_args(rq, **change), ctypes.c_size_t()
     refused(rq, rq.lib().svdq_attention_workspace_size(ctypes.byref(c), ctypes.byref(n)), status, message)
-    refused(rq, rq.lib().svdq_attention_forward(ctypes.byref(c), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 30, None),
-            status, message)
+    refused(rq, rq.lib().svdq_attention_forward(ctypes.byref(c), None), status, message)
 
 
 @pytest.mark.parametrize("q,k,v,qo,ko,out,batch,message", [
@@ -58,14 +58,14 @@ def test_attention_refuses_bad_configurations(rq, change, status, message):
     (FAKE, FAKE, FAKE, None, FAKE, FAKE, 2, b"offsets"), (FAKE, FAKE, FAKE, FAKE, None, FAKE, 2, b"offsets"),
 ])
 def test_attention_refuses_bad_pointers(rq, q, k, v, qo, ko, out, batch, message):
-    c = attention_config(rq, batch=batch)
-    refused(rq, rq.lib().svdq_attention_forward(ctypes.byref(c), q, k, v, qo, ko, out, FAKE, 1 << 30, None), INVALID, message)
-    assert rq.lib().svdq_attention_forward(None, q, k, v, qo, ko, out, FAKE, 1 << 30, None) == INVALID
+    c = attention_args(rq, batch=batch, q=q, k=k, v=v, q_offsets=qo, k_offsets=ko, out=out)
+    refused(rq, rq.lib().svdq_attention_forward(ctypes.byref(c), None), INVALID, message)
+    assert rq.lib().svdq_attention_forward(None, None) == INVALID
     assert rq.lib().svdq_attention_workspace_size(ctypes.byref(c), None) == INVALID
 
 
 @pytest.mark.parametrize("change,status,message", [
-    (dict(dtype=2), INVALID, b"dtype"), (dict(act=5), INVALID, b"activation"), (dict(act=-1), INVALID, b"activation"),
+    (dict(dtype=2), INVALID, b"dtype"), (dict(activation=5), INVALID, b"activation"), (dict(activation=-1), INVALID, b"activation"),
     (dict(M=-1), INVALID, b"M must"), (dict(K=0), INVALID, b"multiples of 8"), (dict(K=12), INVALID, b"multiples of 8"),
     (dict(N=100), INVALID, b"multiples of 8"), (dict(M=1 << 23), UNSUPPORTED, b"exceeds"), (dict(X=None), INVALID, b"NULL"),
     (dict(W=None), INVALID, b"NULL"), (dict(Y=None), INVALID, b"NULL"), (dict(X=FAKE + 2), INVALID, b"aligned"),
@@ -73,9 +73,11 @@ def test_attention_refuses_bad_pointers(rq, q, k, v, qo, ko, out, batch, message
     (dict(residual=FAKE + 2), INVALID, b"aligned"), (dict(Y=FAKE + 8), INVALID, b"aligned"),
 ])
 def test_linear_refuses_bad_arguments(rq, change, status, message):
-    a = dict(dtype=0, X=FAKE, W=FAKE, bias=None, residual=None, act=0, M=4, K=64, N=64, Y=FAKE)
-    a.update(change)
-    refused(rq, rq.lib().svdq_dense_linear_forward(*a.values(), None), status, message)
+    a = rq._DenseLinear(dtype=0, activation=0, M=4, K=64, N=64, X=FAKE, W=FAKE, Y=FAKE)
+    for name, value in change.items():
+        setattr(a, name, value)
+    refused(rq, rq.lib().svdq_dense_linear_forward(ctypes.byref(a), None), status, message)
+    assert rq.lib().svdq_dense_linear_forward(None, None) == INVALID
 
 
 def norm_args(rq, **change):
@@ -105,9 +107,9 @@ def test_norm_refuses_bad_arguments(rq, change, status, message):
 
 
 def test_nothing_to_do_is_no_error(rq):
-    c = attention_config(rq, q_rows=0)
-    assert rq.lib().svdq_attention_forward(ctypes.byref(c), None, None, None, None, None, None, None, 0, None) == 0
-    assert rq.lib().svdq_dense_linear_forward(0, None, None, None, None, 0, 0, 64, 64, None, None) == 0
+    c = attention_args(rq, q_rows=0, q=None, out=None)
+    assert rq.lib().svdq_attention_forward(ctypes.byref(c), None) == 0
+    assert rq.lib().svdq_dense_linear_forward(ctypes.byref(rq._DenseLinear(M=0, K=64, N=64)), None) == 0
     assert rq.lib().svdq_residual_norm(ctypes.byref(norm_args(rq, rows=0, x=None, y=None, x_out=None, h_out=None)), None) == 0
 
 
