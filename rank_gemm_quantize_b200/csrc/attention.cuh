@@ -40,7 +40,7 @@ template <class T>
 struct Half16;
 template <>
 struct Half16<__nv_bfloat16> {
-  static constexpr uint32_t kExp = 0x7F80;  // all exponent bits: infinities and NaN
+  static constexpr uint32_t kExp = 0x7F80;  // the exponent's bits (all of them: infinities and NaN)
   static constexpr uint32_t kFmt = 1;       // operand format code of kind::f16
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -61,19 +61,34 @@ struct Half16<__half> {
   }
 };
 
-// Zeroes the infinities and NaN of eight 16-bit values; true if there were any.
+// Whether any of eight 16-bit values is an infinity or NaN (all exponent bits
+// set: one more in the exponent's last place carries into the sign's).
 template <class T>
-__device__ __forceinline__ bool drop_non_finite(uint4& v) {
+__device__ __forceinline__ bool has_non_finite(const uint4& v) {
+  constexpr uint32_t e = Half16<T>::kExp * 0x10001u, one = (Half16<T>::kExp & -Half16<T>::kExp) * 0x10001u;
+  return (((v.x & e) + one) | ((v.y & e) + one) | ((v.z & e) + one) | ((v.w & e) + one)) & 0x80008000u;
+}
+// Those values become 0.
+template <class T>
+__device__ __forceinline__ void drop_non_finite(uint4& v) {
   uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-  bool any = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     constexpr uint32_t e = Half16<T>::kExp;
-    if ((w[i] & e) == e) w[i] &= 0xFFFF0000u, any = true;
-    if ((w[i] >> 16 & e) == e) w[i] &= 0x0000FFFFu, any = true;
+    if ((w[i] & e) == e) w[i] &= 0xFFFF0000u;
+    if ((w[i] >> 16 & e) == e) w[i] &= 0x0000FFFFu;
   }
-  return any;
 }
+
+__device__ __forceinline__ uint4 load_shared(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_shared(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void store_shared(uint32_t addr, const uint4& v) { store_shared(addr, v.x, v.y, v.z, v.w); }
 
 // 2^x in one instruction (results under the normal range become 0).
 __device__ __forceinline__ float exp2_fast(float x) {

@@ -18,7 +18,7 @@
 // tile's. The exponential unit alone would need 1024 cycles a tile, so three
 // of eight exponentials are computed with multiply-adds (exp2_pair).
 // (Two S of 64 keys a tile would shorten the chain, but an MMA of 64 columns takes
-// as long as one of 128: 302 us where this takes KERNEL us, 4608 x 4608 keys,
+// as long as one of 128: 302 us where this takes 226 us, 4608 x 4608 keys,
 // 24 heads of 128.)
 //
 // O is not rescaled whenever m grows, only when it grew by more than 2^8 since
@@ -29,7 +29,6 @@
 // values that a query must not see out of the product (below). K and V tiles
 // share one ring of stages in the order K0 V0 K1 V1 ..
 #include <string>
-#include <type_traits>
 
 #include "attention.cuh"
 #include "operator_status.cuh"
@@ -103,10 +102,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 // 2^x of two values without the exponential unit: x = i + f, f in [-1/2, 1/2]; the
 // polynomial (minimax in the relative error by Lawson's iteration, 2.6e-6) gives
-// 2^f, and i goes into its exponent. Below -127 as at -127; NaN stays.
+// 2^f, and i goes into its exponent. 0 below 2^-126, as a hidden key needs; NaN stays.
 __device__ __forceinline__ float2 exp2_pair(float2 x) {
-  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));
-  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
   auto both = [](float c) { return make_float2(c, c); };
   const float2 t = __fadd2_rn(x, both(12582912.f));  // 3 2^22: i in the low bits
   const float2 f = __ffma2_rn(__fadd2_rn(t, both(-12582912.f)), both(-1.f), x);
@@ -115,8 +112,9 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
   q = __ffma2_rn(q, f, both(0.240247451f));
   q = __ffma2_rn(q, f, both(0.693121821f));
   q = __ffma2_rn(q, f, both(0.999999262f));
-  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
+  const float a = __uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23));
+  const float b = __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23));
+  return make_float2(x.x < -126.f ? 0.f : a, x.y < -126.f ? 0.f : b);
 }
 
 // Tensor memory: S (and, over it, P) of the two tiles, then the two results.
@@ -184,23 +182,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
     for (int c = 0; c < DP / 64; ++c) tma_load_3d(st + c * 128 * 128, map, bar, c * 64, hk, ks + k_begin + (i >> 1) * kPromptKeys);
   };
   const int ahead = min(2 * n, L::kStages);
-  if (tid == 9 * 32) {  // the load warp: the first loads wait for nothing but the barriers
-    for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&full[s], 2);  // twice by the load warp, or once each by the two that clean the tile
-      mbar_init(&empty[s], 1);
-      mbar_init(&dirty[s], 1);
+  if (warp == 9) {  // the load warp: the first loads wait for nothing but the barriers
+    constexpr int kBarriers = 3 * L::kStages + 8;
+    static_assert(kBarriers <= 32, "a lane a barrier");
+    // two arrivals on `full`: by this warp, or one of each of the two that clean the tile; four warps on p_full
+    if (lane < kBarriers) mbar_init(&full[lane], lane < L::kStages ? 2 : &full[lane] >= p_full && &full[lane] < p_full + 4 ? 4 : 1);
+    if (lane == 0) {
+      *abort_flag = 0;
+      *spoiled = 0;
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t], 1);
-      mbar_init(&o_done[t], 1);
-    }
-    for (int h = 0; h < 4; ++h) mbar_init(&p_full[h], 4);
-    *abort_flag = 0;
-    *spoiled = 0;
     fence_barrier_init();
-    for (int i = 0; i < ahead; ++i) load(i);
+    __syncwarp();
+    if (lane == 0)
+      for (int i = 0; i < ahead; ++i) load(i);
+    __syncwarp();
   }
-  __syncwarp();
   if (warp == 8) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
@@ -221,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
 #pragma unroll
     for (int i = 0; i < 32 / kAtOnce; ++i) {
       const int r = 32 * warp + i * kAtOnce + lane / kLanes;
-      *reinterpret_cast<uint4*>(smem + (r / kTileRows) * L::kQTile + tile_at(r % kTileRows, lane % kLanes)) = v[i];
+      store_shared(smem_u32(smem) + (r / kTileRows) * L::kQTile + tile_at(r % kTileRows, lane % kLanes), v[i]);
     }
   }
   fence_proxy_async_smem();
@@ -335,25 +331,32 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
         uint8_t* st = smem + L::kRing + stage * L::kStage;
         const int key0 = k_begin + j * kPromptKeys;
         bool any = false;
-        constexpr int kPieces = kPromptKeys * (DP / 8) / 64;
+        // a thread's 16-byte pieces lie in the same place of every kApart-th row
+        constexpr int kApart = 64 / (DP / 8), kBatch = 8;
+        const int piece = ((warp - 10) * 32 + lane) % (DP / 8), r0 = ((warp - 10) * 32 + lane) / (DP / 8);
+        const uint32_t tile = smem_u32(st);
 #pragma unroll 1
-        for (int i = 0; i < kPieces; i += 8) {
-          uint4 v[8];
-          uint4* at16[8];
+        for (int r = r0; r < kPromptKeys; r += kBatch * kApart) {
+          uint4 v[kBatch];
+          bool odd = false;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int e = (warp - 10) * 32 + lane + 64 * (i + k);
-            at16[k] = reinterpret_cast<uint4*>(st + tile_at(e / (DP / 8), e % (DP / 8)));
-            v[k] = *at16[k];
+          for (int i = 0; i < kBatch; ++i) v[i] = load_shared(tile + tile_at(r + i * kApart, piece));
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int key = key0 + r + i * kApart;
+            odd |= (key >= kl) | ((key > first_limit) & has_non_finite<T>(v[i]));
           }
+          if (!odd) continue;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int key = key0 + ((warp - 10) * 32 + lane + 64 * (i + k)) / (DP / 8);
-            if (key <= first_limit) continue;
-            if (key >= kl)
-              *at16[k] = make_uint4(0, 0, 0, 0);
-            else if (drop_non_finite<T>(v[k]))
-              *at16[k] = v[k], any = true;
+          for (int i = 0; i < kBatch; ++i) {
+            const int key = key0 + r + i * kApart;
+            if (key >= kl) {
+              v[i] = make_uint4(0, 0, 0, 0);
+            } else if (key > first_limit && has_non_finite<T>(v[i])) {
+              drop_non_finite<T>(v[i]);
+              any = true;
+            }
+            store_shared(tile + tile_at(r + i * kApart, piece), v[i]);
           }
         }
         if (any) *spoiled = 1;
@@ -384,8 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       for (int b = 0; b < 4; ++b) tmem_ld32(scores + 32 * b, s[b]);
       tmem_ld_wait();
       const int key0 = k_begin + j * kStepN;
-      const bool masked = key0 + kStepN - 1 > warp_limit;  // some row does not see some key
-      if (masked) {
+      if (key0 + kStepN - 1 > warp_limit) {  // some row does not see some key
         const int seen = lim - key0;
 #pragma unroll
         for (int b = 0; b < 4; ++b)
@@ -396,15 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       const float2 c2 = make_float2(c, c);
       float2 base2, sum[4];  // a packed sum takes long: several chains of them
       uint32_t pk[2][16];
-      // 64 of the scores to probabilities; where no key is hidden (those need 0
-      // exactly) two of eight pairs go by multiply-adds
-      auto half = [&](int h, auto mixed) {
+      // 64 of the scores to probabilities, two of eight pairs by multiply-adds
+      auto half = [&](int h) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * h + b][2 * e]), __uint_as_float(s[2 * h + b][2 * e + 1])), c2, base2);
-            if (decltype(mixed)::value && (3 * e) % 8 < 2) {
+            if ((3 * e) % 8 < 2) {
               x = exp2_pair(x);
             } else {
               x.x = exp2_fast(x.x);
@@ -451,15 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       base2 = make_float2(-base, -base);
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
-      if (masked)
-        half(0, std::false_type());
-      else
-        half(0, std::true_type());
+      half(0);
       hand_over(0);
-      if (masked)
-        half(1, std::false_type());
-      else
-        half(1, std::true_type());
+      half(1);
       hand_over(1);
 #pragma unroll
       for (int i = 1; i < 4; ++i) sum[0] = __fadd2_rn(sum[0], sum[i]);
@@ -482,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
       const long long place = !write ? -1
                               : split ? static_cast<long long>(slot) * DP
                                       : (static_cast<long long>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim;
-      uint8_t* stage = smem + t * L::kQTile;  // the tile's queries are used up; each warp keeps to its rows
+      const uint32_t stage = smem_u32(smem) + t * L::kQTile;  // the tile's queries are used up; each warp keeps to its rows
 #pragma unroll 1
       for (int b = 0; b < DP; b += 32) {
         uint32_t o[32];
@@ -505,14 +500,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
         if (split) {  // 32 float columns a row at a time: 128 bytes
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(stage + tile_at(32 * (warp & 3) + lane, e)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            store_shared(stage + tile_at(32 * (warp & 3) + lane, e), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = 4 * i + lane / 8;
             const long long to = __shfl_sync(0xffffffffu, place, r);
-            if (to >= 0)
-              *reinterpret_cast<uint4*>(p.part + to + b + 4 * (lane % 8)) = *reinterpret_cast<const uint4*>(stage + tile_at(32 * (warp & 3) + r, lane % 8));
+            const uint4 v = load_shared(stage + tile_at(32 * (warp & 3) + r, lane % 8));
+            if (to >= 0) *reinterpret_cast<uint4*>(p.part + to + b + 4 * (lane % 8)) = v;
           }
           __syncwarp();
         } else {
@@ -521,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
             uint32_t w[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h) w[h] = Half16<T>::pack(__uint_as_float(o[e + 2 * h]) * norm, __uint_as_float(o[e + 2 * h + 1]) * norm);
-            *reinterpret_cast<uint4*>(stage + tile_at(32 * (warp & 3) + lane, (b + e) / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+            store_shared(stage + tile_at(32 * (warp & 3) + lane, (b + e) / 8), w[0], w[1], w[2], w[3]);
           }
         }
       }
@@ -531,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
         uint4 v[32 / kAtOnce];
 #pragma unroll
         for (int i = 0; i < 32 / kAtOnce; ++i)
-          v[i] = *reinterpret_cast<const uint4*>(stage + tile_at(32 * (warp & 3) + i * kAtOnce + lane / kLanes, c));
+          v[i] = load_shared(stage + tile_at(32 * (warp & 3) + i * kAtOnce + lane / kLanes, c));
 #pragma unroll
         for (int i = 0; i < 32 / kAtOnce; ++i) {
           const long long to = __shfl_sync(0xffffffffu, place, i * kAtOnce + lane / kLanes);

@@ -204,8 +204,10 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
           uint4 v = *at16;
           if (key >= kl)
             *at16 = make_uint4(0, 0, 0, 0);
-          else if (drop_non_finite<T>(v))
+          else if (has_non_finite<T>(v)) {
+            drop_non_finite<T>(v);
             *at16 = v, any = true;
+          }
         }
         if (any) spoiled = 1;
         fence_proxy_async_smem();  // the stage is loaded again by TMA
