@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnPara
   __shared__ int sums[kWarps];
   __shared__ float warp_ml[kWarps][2];
   __shared__ float warp_o[kWarps][DP];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before has ended
   const int b = blockIdx.x, hk = blockIdx.y, warp = warp_id(), lane = lane_id();
   const int chunk = key_chunk(p);
   const Shares s = shares_of(p, b, chunk);
@@ -527,11 +528,17 @@ cudaError_t join(const AttnParams& p, cudaStream_t st) {
   const bool wide = p.tile_rows > kStepRows;
   const int z = static_cast<int>(std::min<long long>(wide ? (rows + 3) / 4 : rows, 4096));
   const dim3 grid(p.batch, p.kv_heads, z);
-  if (wide)
-    attention_join_kernel<T, DP, 4><<<grid, kThreads, 0, st>>>(p);
-  else
-    attention_join_kernel<T, DP, 1><<<grid, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  // set up while the shares are computed; the kernel waits for them itself
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return wide ? cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP, 4>, p) : cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP, 1>, p);
 }
 
 }  // namespace
