@@ -6,15 +6,21 @@
 // rows of X. W^T is the tensor core's A operand (the tile [64 k, 128 n] lands by
 // TMA as it lies in memory: M-major), X its B operand, so a product with few
 // rows costs few tensor-core columns and the kernel streams W at memory speed.
-// Where the tiles do not fill the SMs, the CTAs of a cluster take shares
-// of K: each sends its float partial sums of a slice of the rows to the CTA that
-// owns the slice (distributed shared memory), and the owner adds them in a
-// fixed order. No workspace, no atomics, one launch.
+// Where the tiles leave SMs free, the CTAs of a cluster take shares of K: each
+// sends its float partial sums of a slice of the rows to the CTA that owns the
+// slice (distributed shared memory), and the owner adds them in a fixed order.
+// No workspace, no atomics, one launch. W's bytes bound it (1 x 3072 x 18432,
+// 113 MB: 24 us, 72% of a copy's rate), and where W is small the latency of one
+// load, one product and the join (37 x 2056 x 1000: 7 us on the device).
 //
 // Pair kernel (many tiles): two SMs work as one (tcgen05 .cta_group::2) on a
-// 256 x 256 tile, each holding its own 128 rows of X and 128 columns of W.
-// Persistent; two accumulators in tensor memory, so the epilogue of a tile
-// runs under the next tile's products.
+// tile of 256 rows and 256 or 128 columns, each holding its own 128 rows of X and
+// half of W's columns: an SM then loads 32 KB per 512 cycles of products (a
+// tile of its own, 128 x 128, needs as much for 256; an SM takes in 50 to 60 bytes a
+// cycle). Persistent; two accumulators in tensor memory, so the epilogue of a tile
+// runs under the next tile's products. The tensor core bounds it (4608 x 3072 x
+// 12288: 1567 TFLOP/s, and under the power cap of a long run 1298; a library's
+// plain product 1617 and 1338).
 #include <algorithm>
 #include <cstdint>
 #include <string>
@@ -69,7 +75,8 @@ __device__ __forceinline__ float2 gelu2(float2 t) {
   return make_float2(__fdividef(t.x, 1.f + exp2_fast(-g.x)), __fdividef(t.y, 1.f + exp2_fast(-g.y)));
 }
 
-__device__ __forceinline__ void activate(float2 (&v)[4], int act) {
+template <int N>
+__device__ __forceinline__ void activate(float2 (&v)[N], int act) {
   switch (act) {
     case SVDQ_ACT_RELU:
 #pragma unroll
@@ -337,22 +344,23 @@ cudaError_t start_rows(const DenseParams& p, const DenseMaps& maps, int sms, cud
 }
 
 // ---------------------------------------------------------------- pair kernel
-constexpr int kPairM = 256, kPairN = 256;  // tile of a pair of SMs
-constexpr int kEpiWarps = 8;               // two per quarter of the lanes, 128 columns each
+constexpr int kPairM = 256;                // rows of a pair's tile; it has NT columns, 256 or 128
+constexpr int kEpiWarps = 8;               // two per quarter of the lanes, half the columns each
 constexpr int kPairThreads = (2 + kEpiWarps) * 32;
 constexpr int kGroupM = 16;                // row blocks that share the column blocks of W in L2
 
+template <int NT>
 struct PairSmem {
   static constexpr int kX = 128 * kBK * 2;  // this CTA's rows
-  static constexpr int kW = kBK * 128 * 2;  // this CTA's columns
+  static constexpr int kW = kBK * NT;       // this CTA's columns, half of the tile's
   static constexpr int kStage = kX + kW;
-  static constexpr int kStages = 6;
+  static constexpr int kStages = NT == 256 ? 6 : 8;
   static constexpr int kBox = 32 * 64;      // Y on its way out: 32 rows, 32 columns
   static constexpr int kBoxes = kStages * kStage;
   static constexpr int kBars = kBoxes + kEpiWarps * 2 * kBox;
   static constexpr int kTotal = kBars + 512 + 1024;
 };
-static_assert(PairSmem::kTotal <= 232448, "shared memory budget");
+static_assert(PairSmem<256>::kTotal <= 232448 && PairSmem<128>::kTotal <= 232448, "shared memory budget");
 
 __device__ __forceinline__ void pair_tile(int tile, int m_blocks, int n_blocks, int& mb, int& nb) {
   const int group = tile / (kGroupM * n_blocks), first = group * kGroupM, in = tile % (kGroupM * n_blocks);
@@ -361,10 +369,10 @@ __device__ __forceinline__ void pair_tile(int tile, int m_blocks, int n_blocks, 
   nb = in / size;
 }
 
-template <class T>
+template <class T, int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     dense_pair_kernel(const DenseParams p, const __grid_constant__ DenseMaps maps) {
-  using L = PairSmem;
+  using L = PairSmem<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // [kStages] (leader) both CTAs' loads have landed
@@ -378,10 +386,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int m_blocks = (p.M + kPairM - 1) / kPairM, n_blocks = (p.N + kPairN - 1) / kPairN;
+  const int m_blocks = (p.M + kPairM - 1) / kPairM, n_blocks = (p.N + NT - 1) / NT;
   const int tiles = m_blocks * n_blocks, pairs = gridDim.x >> 1;
   const int blocks = (p.K + kBK - 1) / kBK;
 
+  if (warp == 2 && lane < 3) prefetch_tensormap(lane == 0 ? &maps.x : lane == 1 ? &maps.w : &maps.y);
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -396,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, 512);
+    tmem_alloc_pair(tmem_slot, 2 * NT);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -412,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs) {
         int mb, nb;
         pair_tile(tile, m_blocks, n_blocks, mb, nb);
-        const int m = mb * kPairM + static_cast<int>(rank) * 128, n = nb * kPairN + static_cast<int>(rank) * 128;
+        const int m = mb * kPairM + static_cast<int>(rank) * 128, n = nb * NT + static_cast<int>(rank) * (NT / 2);
         for (int k = 0; k < blocks; ++k, ++it) {
           const int s = it % L::kStages;
           ok = mbar_wait(&empty[s], ((it / L::kStages) & 1) ^ 1, abort_flag, &g_status);
@@ -422,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (leader) mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
           tma_load_2d_pair(st, &maps.x, bar, k * kBK, m);
           tma_load_2d_pair(st + L::kX, &maps.w, bar, n, k * kBK);
-          tma_load_2d_pair(st + L::kX + 8192, &maps.w, bar, n + 64, k * kBK);
+          if (NT == 256) tma_load_2d_pair(st + L::kX + 8192, &maps.w, bar, n + 64, k * kBK);
         }
       }
       if (!ok && leader) {  // gave up: the pair's copies in flight land before it ends
@@ -434,30 +443,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMAs (leader)
-    if (leader && lane == 0) {
-      // B: W, 256 columns over the pair, N-major (bit 16)
-      const uint32_t idesc = idesc_dense(kFmtF32, Half16<T>::kFmt, Half16<T>::kFmt, kPairM, kPairN) | (1u << 16);
+    // The whole warp goes through the loops, one lane issues: what an MMA reads then
+    // stays in uniform registers.
+    if (leader) {
+      // B: W, NT columns over the pair, N-major (bit 16)
+      const uint32_t idesc = idesc_dense(kFmtF32, Half16<T>::kFmt, Half16<T>::kFmt, kPairM, NT) | (1u << 16);
+      const bool issues = elect_one();
+      const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0), ring = smem_u32(smem);
+      // all lanes or none: no lane falls behind by two phases
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_status)) != 0;
+      };
       bool ok = true;
       uint32_t it = 0;
       int ti = 0;
       for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += pairs, ++ti) {
         const int b = ti & 1;
-        ok = mbar_wait(&acc_empty[b], ((ti >> 1) & 1) ^ 1, abort_flag, &g_status);
+        ok = wait(&acc_empty[b], ((ti >> 1) & 1) ^ 1);
         if (!ok) break;
         tc_fence_after();
         for (int k = 0; k < blocks; ++k, ++it) {
           const int s = it % L::kStages;
-          ok = mbar_wait(&full[s], (it / L::kStages) & 1, abort_flag, &g_status);
+          ok = wait(&full[s], (it / L::kStages) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t xa = smem_u32(smem + s * L::kStage), wb = xa + L::kX;
+          const uint32_t xa = ring + s * L::kStage, wb = xa + L::kX;
+          if (issues) {
 #pragma unroll
-          for (int e = 0; e < kBK / 16; ++e)
-            mma_f16_pair(tmem + b * kPairN, smem_desc(xa + 32 * e, 16, 1024, kSw128), smem_desc(wb + 2048 * e, 8192, 1024, kSw128),
-                         idesc, (k > 0 || e > 0) ? 1u : 0u);
-          tc_commit_pair_mc(&empty[s], 0x3);
+            for (int e = 0; e < kBK / 16; ++e)
+              mma_f16_pair(base + b * NT, smem_desc(xa + 32 * e, 16, 1024, kSw128), smem_desc(wb + 2048 * e, 8192, 1024, kSw128),
+                           idesc, (k > 0 || e > 0) ? 1u : 0u);
+            tc_commit_pair_mc(&empty[s], 0x3);
+          }
         }
-        if (ok) tc_commit_pair_mc(&acc_full[b], 0x3);
+        if (ok && issues) tc_commit_pair_mc(&acc_full[b], 0x3);
       }
     }
     __syncwarp();
@@ -465,14 +484,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // -------------------------------------------------------------- epilogue (both CTAs)
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* box = smem + L::kBoxes + (warp - 2) * 2 * L::kBox;
-    const T* residual = static_cast<const T*>(p.residual);
+    const T *bias = static_cast<const T*>(p.bias), *residual = static_cast<const T*>(p.residual);
     int ti = 0;
     for (int tile = blockIdx.x >> 1; tile < tiles; tile += pairs, ++ti) {
       int mb, nb;
       pair_tile(tile, m_blocks, n_blocks, mb, nb);
-      const int b = ti & 1, row0 = mb * kPairM + static_cast<int>(rank) * 128 + 32 * q, row = row0 + lane;
-      const int col0 = nb * kPairN + half * 128;
-      const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16) + b * kPairN + half * 128;
+      const int buf = ti & 1, row0 = mb * kPairM + static_cast<int>(rank) * 128 + 32 * q, row = row0 + lane;
+      const int col0 = nb * NT + half * (NT / 2);
+      const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * NT + half * (NT / 2);
+      // a lane holds the bias of NT / 64 columns; shuffles bring them where they are added
+      constexpr int kWords = NT / 128;
+      uint32_t bias_words[kWords] = {};
+      const int bias_col = col0 + 2 * kWords * lane;
+      if (bias && bias_col < p.N) {
+        if constexpr (kWords == 2) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(bias + bias_col));
+          bias_words[0] = w.x, bias_words[1] = w.y;
+        } else {
+          bias_words[0] = __ldg(reinterpret_cast<const uint32_t*>(bias + bias_col));
+        }
+      }
       uint4 r4[4] = {};  // the residual of the next 32 columns
       auto fetch = [&](int c) {
 #pragma unroll
@@ -482,34 +513,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       };
       fetch(0);
-      if (!mbar_wait(&acc_full[b], (ti >> 1) & 1, abort_flag, &g_status)) break;
+      if (!mbar_wait(&acc_full[buf], (ti >> 1) & 1, abort_flag, &g_status)) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
+      for (int c = 0; c < NT / 2; c += 32) {
         uint32_t a[32];
         tmem_ld32(acc + c, a);
-        uint4 r[4] = {r4[0], r4[1], r4[2], r4[3]};
-        if (c + 32 < 128) fetch(c + 32);
+        const uint4 r[4] = {r4[0], r4[1], r4[2], r4[3]};
+        if (c + 32 < NT / 2) fetch(c + 32);
         tmem_ld_wait();
-        if (c + 32 == 128) {  // the sums are in registers: the next tile but one may start
+        if (c + 32 == NT / 2) {  // the sums are in registers: the next tile but one may start
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(&acc_empty[b], 0);
+          if (lane == 0) mbar_arrive_cluster(&acc_empty[buf], 0);
+        }
+        float2 v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = make_float2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
+        if (bias) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            v[e] = __fadd2_rn(v[e], unpack<T>(__shfl_sync(0xffffffffu, bias_words[e % kWords], c / (2 * kWords) + e / kWords)));
+        }
+        activate(v, p.act);
+        if (residual) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint4 w = r[e >> 2];
+            v[e] = __fadd2_rn(v[e], unpack<T>((e & 3) == 0 ? w.x : (e & 3) == 1 ? w.y : (e & 3) == 2 ? w.z : w.w));
+          }
         }
         uint8_t* out = box + ((c >> 5) & 1) * L::kBox + lane * 64;
         if (lane == 0) bulk_wait_group_read<1>();  // the store before the last has read this box
         __syncwarp();
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int n = col0 + c + 8 * v;
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(a[8 * v + e]);
-          uint4 bias = make_uint4(0, 0, 0, 0);
-          if (p.bias && n < p.N) bias = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + n));
-          const uint4 y = finish8<T>(p, bias, x, r[v]);
-          *reinterpret_cast<uint4*>(out + ((v ^ ((lane >> 1) & 3)) << 4)) = y;
-        }
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(out + ((e ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(Half16<T>::pack(v[4 * e].x, v[4 * e].y), Half16<T>::pack(v[4 * e + 1].x, v[4 * e + 1].y),
+                         Half16<T>::pack(v[4 * e + 2].x, v[4 * e + 2].y), Half16<T>::pack(v[4 * e + 3].x, v[4 * e + 3].y));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -518,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
     }
-    if (lane == 0) bulk_wait_group<0>();
+    if (lane == 0) bulk_wait_group_read<0>();
     __syncwarp();
   }
 
@@ -535,19 +576,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(tmem, 2 * NT);
   }
 }
 
-template <class T>
+template <class T, int NT>
 cudaError_t start_pair(const DenseParams& p, const DenseMaps& maps, int sms, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(dense_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairSmem::kTotal);
+    return cudaFuncSetAttribute(dense_pair_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairSmem<NT>::kTotal);
   });
   if (e != cudaSuccess) return e;
-  const long long tiles = static_cast<long long>((p.M + kPairM - 1) / kPairM) * ((p.N + kPairN - 1) / kPairN);
-  dense_pair_kernel<T><<<2 * static_cast<int>(std::min<long long>(tiles, sms / 2)), kPairThreads, PairSmem::kTotal, st>>>(p, maps);
+  const long long tiles = static_cast<long long>((p.M + kPairM - 1) / kPairM) * ((p.N + NT - 1) / NT);
+  dense_pair_kernel<T, NT><<<2 * static_cast<int>(std::min<long long>(tiles, sms / 2)), kPairThreads, PairSmem<NT>::kTotal, st>>>(p, maps);
   return cudaGetLastError();
 }
 
@@ -557,15 +598,19 @@ svdq_status run(const DenseParams& p, const void* X, const void* W, cudaStream_t
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return fail(SVDQ_ERR_CUDA, "no usable current device");
   const CUtensorMapDataType dt = Half16<T>::kFmt == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const long long tiles = static_cast<long long>((p.M + kPairM - 1) / kPairM) * ((p.N + kPairN - 1) / kPairN);
-  const bool pair = p.M > 128 && tiles >= 32;
+  // The rows kernel where its 128 x 128 tiles leave so many SMs free that it can cut
+  // K (256 x 3072 x 3072: 15.8 us, a pair's tiles 17); then tiles of 128 columns
+  // while all pairs' tiles run at once (256 x 3072 x 9216: 19 us, 256 columns 23, the
+  // rows kernel 24), of 256 when not (256 x 3072 x 12288: 24 us, 128 columns 31; rows 44).
+  const long long tiles = static_cast<long long>((p.M + kPairM - 1) / kPairM) * ((p.N + 127) / 128);
+  const bool pair = p.M > 128 && 4 * tiles > sms, wide = tiles > sms / 2;
   const int rb = pair ? 128 : p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
   DenseMaps maps{};
   if (!make_map(&maps.x, dt, X, p.K, p.M, static_cast<uint64_t>(p.K) * 2, kBK, rb, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&maps.w, dt, W, p.N, p.K, static_cast<uint64_t>(p.N) * 2, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B) ||
       (pair && !make_map(&maps.y, dt, p.Y, p.N, p.M, static_cast<uint64_t>(p.N) * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
     return fail(SVDQ_ERR_CUDA, "cuTensorMapEncodeTiled (dense linear) failed");
-  const cudaError_t e = pair       ? start_pair<T>(p, maps, sms, st)
+  const cudaError_t e = pair       ? wide ? start_pair<T, 256>(p, maps, sms, st) : start_pair<T, 128>(p, maps, sms, st)
                         : rb == 16 ? start_rows<T, 16>(p, maps, sms, st)
                         : rb == 32 ? start_rows<T, 32>(p, maps, sms, st)
                         : rb == 64 ? start_rows<T, 64>(p, maps, sms, st)
