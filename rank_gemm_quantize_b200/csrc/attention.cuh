@@ -148,15 +148,15 @@ __device__ __forceinline__ int key_chunk(const AttnParams& p) {
   int longest = keys;
 #pragma unroll
   for (int o = 16; o; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-  int chunk = longest + 1;
-  for (int n = 2; n <= kAutoShares; ++n) {
-    const int c = ((longest + n - 1) / n + 127) & ~127;
-    int ctas = tiles * (keys > c ? (keys + c - 1) / c : 1);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) ctas += __shfl_xor_sync(0xffffffffu, ctas, o);
-    if (c < 512 || ctas > p.fill) break;
-    chunk = c;
+  // lane n tries n + 1 shares of the longest sequence; the last before the first that fails
+  const int c = ((longest + lane) / (lane + 1) + 127) & ~127;
+  int ctas = 0;
+  for (int b = 0; b < p.batch; ++b) {
+    const int k = __shfl_sync(0xffffffffu, keys, b);
+    ctas += __shfl_sync(0xffffffffu, tiles, b) * (k > c ? (k + c - 1) / c : 1);
   }
+  const unsigned fails = __ballot_sync(0xffffffffu, lane > 0 && (c < 512 || ctas > p.fill || lane >= kAutoShares));
+  const int chunk = fails & 2u ? longest + 1 : __shfl_sync(0xffffffffu, c, __ffs(fails) - 2);
   return chunk;
 }
 
