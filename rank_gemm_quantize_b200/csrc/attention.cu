@@ -46,6 +46,8 @@ svdq_status check(const svdq_attention_args* c) {
   return SVDQ_OK;
 }
 
+constexpr int kStepLeast = 512;  // keys of a share (1 x 16000 keys, 4 key heads: 512 17 us, 256 18, 128 28, 1024 19)
+
 struct Plan {
   int sms, chunk, max_slots;
   bool prompt;   // attention_prompt.cu, or attention_step.cu
@@ -66,7 +68,15 @@ svdq_status plan(const svdq_attention_args* c, Plan* out) {
     return fail(SVDQ_ERR_CUDA, "no usable current device");
   }
   const long long rows = static_cast<long long>(c->q_rows) * (c->q_heads / c->kv_heads);
-  p.prompt = rows > 64ll * c->batch;
+  // Eight CTAs an item where all of those run at once, up to 1024 keys each (a lone
+  // token, 4 key heads: of 777 keys 6.1 us, as shares and a join 9.0; of 8000 14.4 and
+  // 14.1; of 16000 24 and 15). Else the kernel for many queries where a sequence
+  // has more than one tile of rows on average, since each reads the keys again (32
+  // rows, 4000 keys, 64 sequences of 8 key heads: 228 us, the kernel for few 262; 16
+  // rows 189 so; 24 rows, 4 sequences: 28 and 26).
+  p.cluster = (rows / kStepRows + c->batch) * c->kv_heads * kStepCluster <= 2 * p.sms &&
+              c->k_rows <= static_cast<long long>(1024) * kStepCluster * c->batch;
+  p.prompt = !p.cluster && rows > static_cast<long long>(kStepRows) * c->batch;
   const int key_tile = p.prompt ? kPromptKeys : kStepKeys, tile_rows = p.prompt ? kPromptRows : kStepRows;
   long long keys, tiles;  // keys of a share; row tiles that can have several shares
   long long slots = -1;
@@ -78,17 +88,18 @@ svdq_status plan(const svdq_attention_args* c, Plan* out) {
     p.open = c->batch <= 32 && tiles < p.fill && c->k_rows > 768;  // of fewer keys no share would have 512
     keys = c->k_rows;
     slots = p.open ? p.fill : 0;
-  } else if ((rows / kStepRows + c->batch) * c->kv_heads * kStepCluster <= 2 * p.sms &&
-             c->k_rows <= static_cast<long long>(1024) * kStepCluster * c->batch) {
-    // all clusters run at once, and their shares of the keys are short
-    p.cluster = true;
+  } else if (p.cluster) {
     tiles = 0;
     keys = c->k_rows;
   } else {
-    // two CTAs an SM, four shares a CTA
+    // Two CTAs an SM. Few sequences: no more shares than run at once, for what a
+    // share costs at its ends (1 x 128000 keys, 4 key heads: 57 us, four a CTA 96). More
+    // sequences: four a CTA, so that uneven lengths even out (64 of 200 to 16000 keys, 8
+    // key heads: 166 us, two a CTA 178, one 214).
     tiles = std::min<long long>(kStepSplitTiles, (rows + kStepRows - 1) / kStepRows);
-    const long long shares = std::max<long long>(1, 8ll * p.sms / c->kv_heads);
-    keys = (c->k_rows + shares - 1) / shares;
+    const long long ctas = 2 * p.sms / c->kv_heads;
+    const long long shares = std::max<long long>(1, 4ll * c->batch <= ctas ? ctas - c->batch : 4 * ctas);
+    keys = std::max<long long>(kStepLeast, (c->k_rows + shares - 1) / shares);
   }
   p.chunk = static_cast<int>(std::max<long long>(1, (keys + key_tile - 1) / key_tile) * key_tile);
   // a sequence of more than `chunk` keys has fewer than 2 keys / chunk shares

@@ -13,20 +13,24 @@
 // their scores, the tensor core multiplies for the other tile; P goes to it in
 // two halves, so that the first is multiplied while the second is computed.
 //
-// A tile's chain of S, softmax and P V is what has to be short: the two tiles'
-// products take 2048 cycles per 128 keys, the softmax may take as long as one
-// tile's. The exponential unit alone would need 1024 cycles a tile, so three
-// of eight exponentials are computed with multiply-adds (exp2_pair).
-// (Two S of 64 keys a tile would shorten the chain, but an MMA of 64 columns takes
-// as long as one of 128: 302 us where this takes 226 us, 4608 x 4608 keys,
-// 24 heads of 128.)
+// A tile's chain of S, softmax and P V bounds it: the two tiles' products take
+// 2048 cycles per 128 keys, a chain 3300 (the softmax 2100 of them, whether the
+// other tile's runs beside it or not). The exponential unit alone would need 1024
+// cycles a tile, so two of eight pairs of exponentials are computed with
+// multiply-adds (exp2_pair). 4608 x 4608 keys, 24 heads of 128: 230 us, 1136
+// TFLOP/s, 70% of a library product's rate; 8192 x 8192, 16 heads of 64: 406 us,
+// 677 TFLOP/s, where the exponentials alone take 240 us. What was slower there:
+// steps of 64 keys with two S a tile (302 us: an MMA of 64 columns takes as long as
+// one of 128), two threads a row (260), P handed over in parts of 32 and 96 keys
+// (232) or 96 and 32 (238), the second half of S loaded under the first's maximum
+// (247), and for heads of 64 P in columns of its own with S issued ahead (463 for 406).
 //
 // O is not rescaled whenever m grows, only when it grew by more than 2^8 since
 // the last time: P may then be up to 2^8 instead of 1, which costs no digits
 // (its relative rounding is the same), and the final division puts it right.
 //
-// Warps: 0-3 and 4-7 the softmax of the two tiles , 8 issues the MMAs, 9 the TMA loads, 10 and 11 keep
-// values that a query must not see out of the product (below). K and V tiles
+// Warps: 0-3 and 4-7 the softmax of the two tiles, 8 issues the MMAs, 9 the TMA loads, 10 and
+// 11 keep values that a query must not see out of the product (below). K and V tiles
 // share one ring of stages in the order K0 V0 K1 V1 ..
 #include <string>
 

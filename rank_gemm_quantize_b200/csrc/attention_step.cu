@@ -14,9 +14,12 @@
 // launch: the eight are a cluster, cut the keys evenly and join their results
 // through distributed shared memory.
 //
-// Memory bounds it: 4 dim bytes a key and key head; 16 rows cost a fraction of
-// the tensor pipe, which is why the narrow mma is used here and a 128-row
-// tensor-memory tile would only add latency.
+// Memory bounds it: 4 dim bytes a key and key head (64 sequences of 200 to 16000
+// keys, 8 key heads of 128, 973 MB: 166 us with the join, 5.9 TB/s, 89% of a copy's
+// rate); 16 rows cost a fraction of the tensor pipe, which is why the narrow mma is
+// used here and a 128-row tensor-memory tile would only add latency. A lone
+// token is latency (777 keys, 4 key heads of 128: 6.1 us on the device; as shares
+// and a join, two launches, 9 us).
 #include <string>
 
 #include "attention.cuh"
@@ -412,38 +415,40 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
 }
 
 // Joins the shares: a row's softmax over all of them. CTA (b, key head, z) takes
-// WIDE rows at a time, z WIDE .., (z + gridDim.z) WIDE ..; 4 / WIDE warps divide a
-// row's shares among them (WIDE 1: few rows of many shares; 4: many of few).
-template <class T, int DP, int WIDE>
-__global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnParams p) {
-  constexpr int kSplit = kWarps / WIDE;
-  __shared__ int sums[kWarps];
-  __shared__ float warp_ml[kWarps][2];
-  __shared__ float warp_o[kWarps][DP];
+// WIDE rows at a time, z WIDE .., (z + gridDim.z) WIDE ..; SPLIT warps divide a row's
+// shares among them.
+template <class T, int DP, int WIDE, int SPLIT>
+__global__ void __launch_bounds__(WIDE * SPLIT * 32) attention_join_kernel(const AttnParams p) {
+  constexpr int kJoinWarps = WIDE * SPLIT;
+  __shared__ int sums[kJoinWarps];
+  __shared__ float warp_ml[kJoinWarps][2];
+  __shared__ float warp_o[kJoinWarps][DP];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before has ended
   const int b = blockIdx.x, hk = blockIdx.y, warp = warp_id(), lane = lane_id();
   const int chunk = key_chunk(p);
   const Shares s = shares_of(p, b, chunk);
   if (!s.slots) return;
   int before = 0;
-  for (int j = threadIdx.x; j < b; j += kThreads) before += shares_of(p, j, chunk).slots;
+  for (int j = threadIdx.x; j < b; j += kJoinWarps * 32) before += shares_of(p, j, chunk).slots;
   before = __shfl_sync(0xffffffffu, warp_inclusive(before), 31);
   if (lane == 0) sums[warp] = before;
   __syncthreads();
-  before = sums[0] + sums[1] + sums[2] + sums[3];
+  before = 0;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) before += sums[w];
   if (before + s.slots > p.max_slots) return;
   int qs, ql;
   seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
   constexpr int kPer = DP / 32;
   const int rows = ql * p.group;
   for (int row0 = blockIdx.z * WIDE; row0 < rows; row0 += gridDim.z * WIDE) {
-    const int row = min(row0 + warp / kSplit, rows - 1);
+    const int row = min(row0 + warp / SPLIT, rows - 1);
     const int first = before + row / p.tile_rows * s.chunks, r = row % p.tile_rows;
     float top = -INFINITY, total = 0.f, o[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[e] = 0.f;
 #pragma unroll 4
-    for (int c = warp % kSplit; c < s.chunks; c += kSplit) {
+    for (int c = warp % SPLIT; c < s.chunks; c += SPLIT) {
       const size_t slot = (static_cast<size_t>(first + c) * p.kv_heads + hk) * p.tile_rows + r;
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot);
       float v[kPer];
@@ -456,7 +461,8 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnPara
 #pragma unroll
       for (int e = 0; e < kPer; ++e) o[e] = fmaf(o[e], was, v[e] * w);
     }
-    if constexpr (kSplit > 1) {
+    if constexpr (SPLIT > 1) {
+      static_assert(WIDE == 1, "the first warp finishes the row");
       if (lane == 0) {
         warp_ml[warp][0] = top;
         warp_ml[warp][1] = total;
@@ -466,13 +472,13 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnPara
       __syncthreads();
       top = -INFINITY;
 #pragma unroll
-      for (int a = 0; a < kSplit; ++a) top = fmaxf(top, warp_ml[a][0]);
+      for (int a = 0; a < SPLIT; ++a) top = fmaxf(top, warp_ml[a][0]);
       const float base = (top == -INFINITY ? 0.f : top) * p.scale_log2;
       total = 0.f;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) o[e] = 0.f;
 #pragma unroll
-      for (int a = 0; a < kSplit; ++a) {
+      for (int a = 0; a < SPLIT; ++a) {
         const float w = exp2_fast(fmaf(warp_ml[a][0], p.scale_log2, -base));
         total = fmaf(warp_ml[a][1], w, total);
 #pragma unroll
@@ -524,21 +530,25 @@ cudaError_t start(const AttnParams& p, const AttnMaps& maps, int sms, cudaStream
 
 template <class T, int DP>
 cudaError_t join(const AttnParams& p, cudaStream_t st) {
+  // Tiles of many rows have few shares (key_chunk): a warp a row. Of few rows, each has
+  // up to hundreds: four warps a row, or 16 (one token, 250 shares: 18 us with the
+  // shares themselves, 39 with four warps).
   const long long rows = (static_cast<long long>(p.q_rows) * p.group + p.batch - 1) / p.batch;
-  const bool wide = p.tile_rows > kStepRows;
+  const bool wide = p.tile_rows > kStepRows, many = !wide && p.k_rows / p.chunk > 16 * p.batch;
   const int z = static_cast<int>(std::min<long long>(wide ? (rows + 3) / 4 : rows, 4096));
-  const dim3 grid(p.batch, p.kv_heads, z);
   // set up while the shares are computed; the kernel waits for them itself
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(p.batch, p.kv_heads, z);
+  cfg.blockDim = dim3(many ? 512 : 128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP, 4>, p) : cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP, 1>, p);
+  return wide   ? cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP, 4, 1>, p)
+         : many ? cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP, 1, 16>, p)
+                : cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP, 1, 4>, p);
 }
 
 }  // namespace
