@@ -421,22 +421,32 @@ template <class T, int DP, int WIDE, int SPLIT>
 __global__ void __launch_bounds__(WIDE * SPLIT * 32) attention_join_kernel(const AttnParams p) {
   constexpr int kJoinWarps = WIDE * SPLIT;
   __shared__ int sums[kJoinWarps];
+  __shared__ Shares own;
   __shared__ float warp_ml[kJoinWarps][2];
   __shared__ float warp_o[kJoinWarps][DP];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before has ended
   const int b = blockIdx.x, hk = blockIdx.y, warp = warp_id(), lane = lane_id();
-  const int chunk = key_chunk(p);
-  const Shares s = shares_of(p, b, chunk);
-  if (!s.slots) return;
+  // the sequence's shares and the slots before its own: up to 32 sequences by the
+  // first warp, since the others have the same to find
+  Shares s{0, 0, 0};
   int before = 0;
-  for (int j = threadIdx.x; j < b; j += kJoinWarps * 32) before += shares_of(p, j, chunk).slots;
-  before = __shfl_sync(0xffffffffu, warp_inclusive(before), 31);
-  if (lane == 0) sums[warp] = before;
+  if (p.batch > 32 || warp == 0) {
+    const int chunk = key_chunk(p), step = p.batch > 32 ? kJoinWarps * 32 : 32;
+    s = shares_of(p, b, chunk);
+    if (s.slots)
+      for (int j = threadIdx.x; j < b; j += step) before += shares_of(p, j, chunk).slots;
+    before = __reduce_add_sync(0xffffffffu, before);
+  }
+  if (lane == 0) {
+    sums[warp] = before;
+    if (warp == 0) own = s;
+  }
   __syncthreads();
+  s = own;
   before = 0;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) before += sums[w];
-  if (before + s.slots > p.max_slots) return;
+  if (!s.slots || before + s.slots > p.max_slots) return;
   int qs, ql;
   seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
   constexpr int kPer = DP / 32;
