@@ -360,7 +360,7 @@ typedef struct {
   int q_heads, kv_heads;   /* q_heads a multiple of kv_heads, at most 128 times it */
   int head_dim;            /* a multiple of 8, 8..128 */
   int causal;              /* 0 or 1 */
-  float scale;             /* positive and finite */
+  float scale;             /* positive, at most 1e30 */
   /* elements from one row (token) to the next and from one head to the next;
      multiples of 8. The values of a head are contiguous. out is contiguous
      [q_rows, q_heads, head_dim]. */

@@ -2,7 +2,6 @@
 // of the kernel and of the shares the keys are cut into.
 #include <algorithm>
 #include <climits>
-#include <cmath>
 #include <string>
 
 #include "attention.cuh"
@@ -34,7 +33,7 @@ svdq_status check(const svdq_attention_args* c) {
   if (c->head_dim < 8 || c->head_dim > 128 || c->head_dim % 8)
     return fail(SVDQ_ERR_INVALID_ARG, "head_dim must be a multiple of 8, 8 to 128");
   if (c->causal != 0 && c->causal != 1) return fail(SVDQ_ERR_INVALID_ARG, "causal must be 0 or 1");
-  if (!(c->scale > 0.f) || !std::isfinite(c->scale)) return fail(SVDQ_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (!(c->scale > 0.f) || c->scale > 1e30f) return fail(SVDQ_ERR_INVALID_ARG, "scale must be positive, at most 1e30");
   // rows and row-head pairs are counted in int
   if (static_cast<long long>(c->q_rows) * c->q_heads > 1ll << 30 || c->k_rows > 1 << 30)
     return fail(SVDQ_ERR_UNSUPPORTED, "q_rows x q_heads or k_rows exceeds 2^30");

@@ -288,3 +288,64 @@ def test_long_cache_passes_31_bits_of_offset():
     o = rq.attention(q, k, v, torch.tensor([0, 1, 1, 2], dtype=torch.int32).cuda(),
                      torch.tensor([0, 500, rows - 700, rows], dtype=torch.int32).cuda(), causal=True)
     ops.check(o, *ops.attention(q, kk, vv, [1, 1], [500, 700], True))
+
+
+# Twenty key heads are too many for one cluster an item: small sizes in the kernels that larger calls take.
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (72, F16), (128, BF16)])
+@pytest.mark.parametrize("q_lengths,k_lengths", [([1, 1], [1, 64]), ([1, 8, 3], [0, 65, 700]), ([17], [17]), ([8], [9]),
+                                                 ([130, 0, 255], [131, 5, 255]), ([256, 257], [256, 400]),
+                                                 ([40, 3, 129], [640, 1200, 129]), ([1] * 6, [3000, 5, 900, 64, 0, 513])])
+def test_many_key_heads(q_lengths, k_lengths, dim, dtype, causal):
+    check(30, q_lengths, k_lengths, 40, 20, dim, dtype, causal)
+
+
+@pytest.mark.parametrize("before", [30, 900])
+@pytest.mark.parametrize("q_lengths", [[1, 1, 1], [150, 300, 70], [3, 40, 3]])
+def test_what_a_query_does_not_see_with_many_key_heads(q_lengths, before):
+    k_lengths = [n + before for n in q_lengths]
+    q, k, v = make(31, q_lengths, k_lengths, 40, 20, 64, BF16)
+    a, b = k_lengths[0], k_lengths[0] + k_lengths[1]
+    k[a:b] = float("nan")
+    v[a:b] = float("inf")
+    v[a - 1, 0, 3] = float("inf")
+    v[a - 1, 19, 5] = float("nan")
+    v[-2, 1, 1] = float("-inf")
+    v[-1, 1, 2] = float("nan")
+    o = run(q, k, v, q_lengths, k_lengths, True)
+    n, m = q_lengths[0], q_lengths[0] + q_lengths[1]
+    assert o[n:m].isnan().all()
+    ops.check(o[:n], *ops.attention(q[:n], k[:a], v[:a], [n], [a], True))
+    ops.check(o[m:], *ops.attention(q[m:], k[b:], v[b:], [q_lengths[2]], [k_lengths[2]], True))
+
+
+@pytest.mark.parametrize("q_lengths,k_lengths", [([5, 200], [2, 60]), ([3, 1], [0, 9]), ([300, 2], [1, 1])])
+def test_queries_that_see_no_key_with_many_key_heads(q_lengths, k_lengths):
+    q, k, v = make(32, q_lengths, k_lengths, 40, 20, 64, BF16)
+    o = run(q, k, v, q_lengths, k_lengths, True)
+    ops.check(o, *ops.attention(q, k, v, q_lengths, k_lengths, True))
+    at = 0
+    for n, m in zip(q_lengths, k_lengths):
+        assert not o[at:at + max(0, n - m)].count_nonzero()
+        at += n
+
+
+@pytest.mark.parametrize("q_lengths,k_lengths", [([300], [3000]), ([1, 1, 1], [9000, 2, 700]), ([1] * 5, [20000, 1, 700, 64, 3])])
+def test_shares_and_join_in_a_graph(q_lengths, k_lengths):
+    """Replayed on new inputs and on new lengths of the same totals."""
+    import rank_gemm_quantize_b200 as rq
+    q, k, v = make(33, q_lengths, k_lengths, 16, 8, 128, BF16)
+    qo, ko = offsets(q_lengths), offsets(k_lengths)
+    rq.attention(q, k, v, qo, ko, causal=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = rq.attention(q, k, v, qo, ko, causal=True)
+    for seed, turned in ((34, False), (35, True), (36, True)):
+        k2 = k_lengths[::-1] if turned else k_lengths
+        for t, n in zip((q, k, v), make(seed, q_lengths, k_lengths, 16, 8, 128, BF16)):
+            t.copy_(n)
+        ko.copy_(offsets(k2))
+        graph.replay()
+        torch.cuda.synchronize()
+        ops.check(o, *ops.attention(q, k, v, q_lengths, k2, True))
+    assert rq.operator_status() == rq.Status.OK

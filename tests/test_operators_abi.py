@@ -40,7 +40,7 @@ def attention_args(rq, **change):
     (dict(q_heads=258, kv_heads=2), INVALID, b"128 times"), (dict(head_dim=0), INVALID, b"head_dim"),
     (dict(head_dim=60), INVALID, b"head_dim"), (dict(head_dim=136), INVALID, b"head_dim"), (dict(causal=2), INVALID, b"causal"),
     (dict(scale=0.0), INVALID, b"scale"), (dict(scale=-1.0), INVALID, b"scale"), (dict(scale=float("nan")), INVALID, b"scale"),
-    (dict(scale=float("inf")), INVALID, b"scale"), (dict(q_rows=1 << 29), UNSUPPORTED, b"2^30"),
+    (dict(scale=float("inf")), INVALID, b"scale"), (dict(scale=1e31), INVALID, b"scale"), (dict(q_rows=1 << 29), UNSUPPORTED, b"2^30"),
     (dict(q_row_stride=100), INVALID, b"strides"), (dict(k_row_stride=0), INVALID, b"strides"),
     (dict(v_head_stride=-64), INVALID, b"strides"), (dict(k_head_stride=1 << 38), INVALID, b"strides"),
 ])
