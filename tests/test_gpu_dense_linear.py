@@ -143,3 +143,43 @@ def test_nothing_to_do():
     import rank_gemm_quantize_b200 as rq
     X, W, b, r = make(10, 0, 64, 64, BF16)
     assert rq.linear(X, W, b, "relu", r).shape == (0, 64)
+
+
+# More than 37 tiles of 256 x 128 go to pairs of SMs, more than 74 in tiles of 256 columns.
+PAIRS = [(1030, 264, 1000), (10000, 72, 8), (300, 136, 2600), (20000, 64, 8), (2600, 200, 1032)]
+
+
+@pytest.mark.parametrize("activation", [None, "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("M,K,N", PAIRS)
+@pytest.mark.parametrize("dtype,bias,residual", [(BF16, True, True), (F16, False, False), (BF16, True, False), (F16, False, True)])
+def test_pairs(M, K, N, dtype, activation, bias, residual):
+    check(21, M, K, N, dtype, activation, bias, residual)
+
+
+@pytest.mark.parametrize("M,K,N", PAIRS)
+def test_pairs_in_place_in_a_graph_with_infinities(M, K, N):
+    import rank_gemm_quantize_b200 as rq
+    X, W, b, r = make(22, M, K, N, BF16)
+    X[3, 5] = float("inf")
+    X[M - 1, 0] = float("nan")
+    r[7, 5] = float("-inf")
+    start, want = r.clone(), ops.linear(X, W, b, "relu", r)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rq.linear(X, W, b, "relu", r, out=r)
+    for _ in range(2):
+        r.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+        ops.check(r, *want)
+
+
+@pytest.mark.parametrize("M,K,N", PAIRS)
+def test_what_lies_around_the_output_of_pairs_stays(M, K, N):
+    import rank_gemm_quantize_b200 as rq
+    X, W, b, _ = make(23, M, K, N, BF16)
+    around = torch.full((M + 300, N), 3.0, dtype=BF16, device="cuda")
+    rq.linear(X, W, b, out=around[:M])
+    torch.cuda.synchronize()
+    ops.check(around[:M], *ops.linear(X, W, b, None, None))
+    assert (around[M:] == 3).all()
