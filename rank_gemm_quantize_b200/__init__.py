@@ -511,10 +511,12 @@ def _operand(name: str, t: torch.Tensor, dtype: torch.dtype, device: int, shape:
     return t.data_ptr()
 
 
-def _offsets(name: str, t: torch.Tensor, device: int) -> int:
-    if t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 1 or t.shape[0] < 2 or not t.is_contiguous():
+def _offsets(name: str, t: torch.Tensor, device: int):
+    """The address of the offsets, and of how many sequences they are."""
+    n = t.numel()
+    if t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 1 or n < 2 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 [sequences + 1] tensor on cuda:{device}")
-    return t.data_ptr()
+    return t.data_ptr(), n - 1
 
 
 def _call_stream(device: int, stream, *made: torch.Tensor) -> int:
@@ -581,14 +583,14 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opti
             return attention(q, k, v, q_offsets, k_offsets, causal, scale, out, workspace, stream)
     batch, qo, ko = 1, 0, 0
     if q_offsets is not None:
-        qo, batch = _offsets("q_offsets", q_offsets, device), q_offsets.shape[0] - 1
+        qo, batch = _offsets("q_offsets", q_offsets, device)
         if k_offsets is None:
             if q.shape[0] != k.shape[0]:
                 raise ValueError("k has other rows than q: k_offsets are needed")
             ko = qo
         else:
-            ko = _offsets("k_offsets", k_offsets, device)
-            if k_offsets.shape[0] != batch + 1:
+            ko, k_batch = _offsets("k_offsets", k_offsets, device)
+            if k_batch != batch:
                 raise ValueError("q_offsets and k_offsets must be of the same length")
     elif k_offsets is not None:
         raise ValueError("k_offsets need q_offsets")
@@ -640,7 +642,7 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     r = 0 if residual is None else _operand("residual", residual, dtype, device, (M, N))
     made = None
     if out is None:
-        out = made = X.new_empty((M, N))
+        out = made = X.new_empty((M, N)) if residual is None else torch.empty_like(residual)
         y = out.data_ptr()
     else:
         y = _operand("out", out, dtype, device, (M, N))
@@ -669,12 +671,13 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
     (the first norm of a model) x' is x itself and only h is computed, in `dtype`
     (that of x where x is not float32); with norm None h is None. out_x may be x,
     out_h may be y. Rows that belong to no sequence are not written."""
-    if x.dim() != 2 or x.dtype not in _DTYPE:
+    x_kind = x.dtype
+    if x.dim() != 2 or x_kind not in _DTYPE:
         raise ValueError("x must be a [rows, dim] tensor of bfloat16, float16 or float32")
     if norm not in _NORM or post_norm not in _NORM:
         raise ValueError(f"unknown norm {norm if norm not in _NORM else post_norm!r}")
-    kind = y.dtype if y is not None else dtype if dtype is not None else x.dtype
-    if kind not in (torch.bfloat16, torch.float16) or x.dtype not in (kind, torch.float32):
+    kind = y.dtype if y is not None else dtype if dtype is not None else x_kind
+    if (kind is not torch.bfloat16 and kind is not torch.float16) or (x_kind is not kind and x_kind is not torch.float32):
         raise ValueError("y and h must be bfloat16 or float16, x of the same type or float32")
     if dtype is not None and dtype != kind:
         raise ValueError("dtype must be that of y")
@@ -688,10 +691,9 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
         raise ValueError("x must be contiguous")
     shape = x.shape
     rows, dim = shape
-    x_kind = x.dtype
     seqs, off, made_x, made_h, x_out, h_out = 1, None, None, None, 0, 0
     if offsets is not None:
-        off, seqs = _offsets("offsets", offsets, device), offsets.shape[0] - 1
+        off, seqs = _offsets("offsets", offsets, device)
     of_row, of_seq = (dim,), (seqs, dim)
     if seqs == 1:  # one row for all may come without its first dimension
         gate, scale, shift = (None if t is None else t.view(1, -1) if t.dim() == 1 else t for t in (gate, scale, shift))
@@ -705,7 +707,7 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
         raise ValueError("without y there is no out_x")
     if norm is not None:
         if out_h is None:
-            out_h = made_h = torch.empty_like(x, dtype=kind)
+            out_h = made_h = torch.empty_like(x, dtype=kind) if y is None else torch.empty_like(y)
             h_out = out_h.data_ptr()
         else:
             h_out = _operand("out_h", out_h, kind, device, shape)

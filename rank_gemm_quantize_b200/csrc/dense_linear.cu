@@ -10,8 +10,8 @@
 // sends its float partial sums of a slice of the rows to the CTA that owns the
 // slice (distributed shared memory), and the owner adds them in a fixed order.
 // No workspace, no atomics, one launch. W's bytes bound it (1 x 3072 x 18432,
-// 113 MB: 24 us, 72% of a copy's rate), and where W is small the latency of one
-// load, one product and the join (37 x 2056 x 1000: 7 us on the device).
+// 113 MB: 21.4 us, 81% of a copy's rate), and where W is small the latency of one
+// load, one product and the join (37 x 2056 x 1000: 6.7 us on the device).
 //
 // Pair kernel (many tiles): two SMs work as one (tcgen05 .cta_group::2) on a
 // tile of 256 rows and 256 or 128 columns, each holding its own 128 rows of X and
@@ -160,7 +160,9 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, float v) {
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// That the barriers of this CTA are there, which fence_barrier_init has published (a
+// releasing arrival: 37 x 2056 x 1000 7.2 us for 6.7).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <class T, int RB>
@@ -614,9 +616,9 @@ svdq_status run(const DenseParams& p, const void* X, const void* W, cudaStream_t
     return fail(SVDQ_ERR_CUDA, "no usable current device");
   const CUtensorMapDataType dt = Half16<T>::kFmt == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   // The rows kernel where its 128 x 128 tiles leave so many SMs free that it can cut
-  // K (256 x 3072 x 3072: 15.8 us, a pair's tiles 17); then tiles of 128 columns
-  // while all pairs' tiles run at once (256 x 3072 x 9216: 19 us, 256 columns 23, the
-  // rows kernel 24), of 256 when not (256 x 3072 x 12288: 24 us, 128 columns 31; rows 44).
+  // K (256 x 3072 x 3072: 15.0 us, a pair's tiles 16); then tiles of 128 columns
+  // while all pairs' tiles run at once (256 x 3072 x 9216: 17 us, 256 columns 21, the
+  // rows kernel 24), of 256 when not (256 x 3072 x 12288: 22 us, 128 columns 28; rows 43).
   const long long tiles = static_cast<long long>((p.M + kPairM - 1) / kPairM) * ((p.N + 127) / 128);
   const bool pair = p.M > 128 && 4 * tiles > sms, wide = tiles > sms / 2;
   const int rb = pair ? 128 : p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
