@@ -1,7 +1,6 @@
 // Host side of the attention calls: argument checks, tensor maps, the choice
 // of the kernel and of the shares the keys are cut into.
 #include <algorithm>
-#include <climits>
 #include <string>
 
 #include "attention.cuh"
@@ -45,10 +44,8 @@ svdq_status check(const svdq_attention_args* c) {
   return SVDQ_OK;
 }
 
-constexpr int kStepLeast = 512;  // keys of a share (1 x 16000 keys, 4 key heads: 512 17 us, 256 18, 128 28, 1024 19)
-
 struct Plan {
-  int sms, chunk, max_slots;
+  int sms, chunk, max_slots, ctas;
   bool prompt;   // attention_prompt.cu, or attention_step.cu
   bool cluster;  // attention_step.cu: an item's shares are a cluster
   bool open;     // attention_prompt.cu: the kernel sets `chunk`
@@ -77,32 +74,25 @@ svdq_status plan(const svdq_attention_args* c, Plan* out) {
               c->k_rows <= static_cast<long long>(1024) * kStepCluster * c->batch;
   p.prompt = !p.cluster && rows > static_cast<long long>(kStepRows) * c->batch;
   const int key_tile = p.prompt ? kPromptKeys : kStepKeys, tile_rows = p.prompt ? kPromptRows : kStepRows;
-  long long keys, tiles;  // keys of a share; row tiles that can have several shares
-  long long slots = -1;
+  long long keys, slots = 0;  // keys of a share; partial results
   if (p.prompt) {
     // where the row tiles alone leave SMs idle, the kernel cuts the keys (key_chunk);
     // its shares are no more than the CTAs that run at once
-    tiles = rows / kPromptRows;
+    const long long tiles = rows / kPromptRows;
     p.fill = p.sms / c->kv_heads;
     p.open = c->batch <= 32 && tiles < p.fill && c->k_rows > 768;  // of fewer keys no share would have 512
     keys = c->k_rows;
     slots = p.open ? p.fill : 0;
   } else if (p.cluster) {
-    tiles = 0;
     keys = c->k_rows;
   } else {
-    // Two CTAs an SM. Few sequences: no more shares than run at once, for what a
-    // share costs at its ends (1 x 128000 keys, 4 key heads: 57 us, four a CTA 96). More
-    // sequences: four a CTA, so that uneven lengths even out (64 of 200 to 16000 keys, 8
-    // key heads: 166 us, two a CTA 178, one 214).
-    tiles = std::min<long long>(kStepSplitTiles, (rows + kStepRows - 1) / kStepRows);
-    const long long ctas = 2 * p.sms / c->kv_heads;
-    const long long shares = std::max<long long>(1, 4ll * c->batch <= ctas ? ctas - c->batch : 4 * ctas);
-    keys = std::max<long long>(kStepLeast, (c->k_rows + shares - 1) / shares);
+    // two CTAs an SM, no more than there are stretches (Line) that are worth one
+    const long long units = rows / kStepRows + c->batch;
+    p.ctas = static_cast<int>(std::min(std::max(1ll, 2ll * p.sms / c->kv_heads), units + c->k_rows / (Line::kLeast * kStepKeys)));
+    keys = c->k_rows;
+    slots = 2ll * p.ctas;
   }
   p.chunk = static_cast<int>(std::max<long long>(1, (keys + key_tile - 1) / key_tile) * key_tile);
-  // a sequence of more than `chunk` keys has fewer than 2 keys / chunk shares
-  if (slots < 0) slots = c->k_rows > p.chunk ? 2ll * c->k_rows / p.chunk * tiles : 0;
   if ((slots + rows / tile_rows + c->batch) * c->kv_heads > 0x7fffffffll) return fail(SVDQ_ERR_UNSUPPORTED, "too many sequences times heads");
   p.max_slots = static_cast<int>(slots);
   const size_t slot_rows = static_cast<size_t>(slots) * c->kv_heads * tile_rows;
@@ -167,9 +157,9 @@ svdq_status svdq_attention_forward(const svdq_attention_args* a, void* stream) {
   p.v_row = a->v_row_stride;
   p.v_head = a->v_head_stride;
   p.tile_rows = pl.prompt ? kPromptRows : kStepRows;
-  p.split_tiles = pl.prompt ? INT_MAX : kStepSplitTiles;
   p.chunk = pl.open ? 0 : pl.chunk;
   p.fill = pl.fill;
+  p.ctas = pl.ctas;
   p.max_slots = pl.max_slots;
   p.part = static_cast<float*>(a->workspace);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + pl.ml);

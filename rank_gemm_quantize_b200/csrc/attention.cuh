@@ -15,10 +15,11 @@ struct AttnParams {
   float scale_log2;   // scale * log2(e): softmax in base 2
   long long q_row, q_head, v_row, v_head;  // strides in elements
   // A sequence's rows (query * group + head in the group) are cut into tiles of
-  // tile_rows, its keys into shares of `chunk` (a multiple of the key tile; 0: see
-  // key_chunk) where it has at most split_tiles row tiles.
-  int tile_rows, split_tiles, chunk;
+  // tile_rows, for attention_prompt.cu its keys into shares of `chunk` (a multiple of
+  // the key tile; 0: see key_chunk).
+  int tile_rows, chunk;
   int fill;           // with chunk 0: CTAs a key head that run at once
+  int ctas;           // attention_step.cu: CTAs a key head
   int max_slots;      // partial results (tile_rows rows each) the workspace holds
   float *part, *part_ml;
 };
@@ -115,7 +116,7 @@ __device__ __forceinline__ Shares shares_of(const AttnParams& p, int b, int chun
   seq_extent(p.k_offsets, b, p.k_rows, ks, kl);
   Shares s;
   s.tiles = (ql * p.group + p.tile_rows - 1) / p.tile_rows;
-  s.chunks = s.tiles <= p.split_tiles && kl > chunk ? (kl + chunk - 1) / chunk : 1;
+  s.chunks = kl > chunk ? (kl + chunk - 1) / chunk : 1;
   s.slots = s.chunks > 1 ? s.tiles * s.chunks : 0;
   return s;
 }
@@ -230,15 +231,130 @@ __device__ bool find_item(const AttnParams& p, Search& at, int idx, Found* share
   return false;
 }
 
-// Few queries (attention_step.cu): row and key tiles; sequences of at most
-// this many row tiles have their keys split.
+// Few queries (attention_step.cu): row and key tiles.
 constexpr int kStepRows = 16;
 constexpr int kStepKeys = 64;
-constexpr int kStepSplitTiles = 4;
 constexpr int kStepCluster = 8;  // CTAs of an item that join within a cluster
 // Many queries (attention_prompt.cu): rows of a CTA (two tensor-memory tiles), key tile.
 constexpr int kPromptRows = 256;
 constexpr int kPromptKeys = 128;
+
+// The work of attention_step.cu as a line: each row tile of each sequence is a unit of
+// kEnds places, for what it costs to begin and end one, and one for each of its key tiles
+// (one at least); unit after unit. Each CTA takes an equal stretch, so that they end
+// together whatever the lengths are, and only the units at a stretch's ends are in
+// parts: the part that begins a unit goes to slot 2 cta + 1, any other to slot 2 cta.
+// (64 tokens on 200 to 16000 keys, 8 key heads: 156 us; shares of equal length dealt
+// out in turn 168. 16 on 4000 each: 50 and 57; on 1000 each 16.4 and 15.0. kEnds 2:
+// 160 us, 8: 160. kLeast 8: 20 tokens on 30 to 12000 keys, 4 key heads, 15.8 us, 5: 14.0.)
+struct Line {
+  long long places;  // of all units
+  long long before;  // ... before sequence b
+  int ctas;          // that share it: one a unit and one per kLeast key tiles, as far as they go
+  static constexpr int kLeast = 5, kEnds = 4;
+  __device__ __forceinline__ long long begin(int cta) const { return places * cta / ctas; }
+  __device__ __forceinline__ int cta_of(long long place) const { return static_cast<int>(((place + 1) * ctas - 1) / places); }
+};
+struct Units {
+  int units;        // row tiles of a sequence
+  int tiles;        // key tiles of each
+};
+__device__ __forceinline__ Units units_of(const AttnParams& p, int b) {
+  int start, ql, kl;
+  seq_extent(p.q_offsets, b, p.q_rows, start, ql);
+  seq_extent(p.k_offsets, b, p.k_rows, start, kl);
+  return {(ql * p.group + kStepRows - 1) / kStepRows, max(1, (kl + kStepKeys - 1) / kStepKeys)};
+}
+// Sum of values from 0 to 2^50 over the warp, in two parts of 24 and 26 bits.
+__device__ __forceinline__ long long warp_sum(long long v) {
+  const unsigned low = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v & 0xFFFFFF));
+  const unsigned high = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v >> 24));
+  return (static_cast<long long>(high) << 24) + low;
+}
+// Called by the whole CTA; `sums` is in shared memory.
+template <int WARPS>
+__device__ __forceinline__ Line line_of(const AttnParams& p, int b, long long (*sums)[3]) {
+  long long v[3] = {0, 0, 0};  // places, those before b, units
+  const bool alone = p.batch <= 32;  // each warp for itself, no barrier
+  for (int j = alone ? lane_id() : threadIdx.x; j < p.batch; j += alone ? 32 : WARPS * 32) {
+    const Units u = units_of(p, j);
+    const long long places = static_cast<long long>(u.units) * (u.tiles + Line::kEnds);
+    v[0] += places;
+    if (j < b) v[1] += places;
+    v[2] += u.units;
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i) v[i] = warp_sum(v[i]);
+  if (!alone) {
+    if (lane_id() == 0)
+      for (int i = 0; i < 3; ++i) sums[warp_id()][i] = v[i];
+    __syncthreads();
+    v[0] = v[1] = v[2] = 0;
+    for (int w = 0; w < WARPS; ++w)
+      for (int i = 0; i < 3; ++i) v[i] += sums[w][i];
+    __syncthreads();
+  }
+  return {v[0], v[1], static_cast<int>(min(static_cast<long long>(p.ctas), v[2] + (v[0] - v[2] * Line::kEnds) / Line::kLeast))};
+}
+struct Part {
+  int b, unit;       // sequence, row tile
+  int place, tiles;  // the place in the unit, and its key tiles
+};
+struct LineSearch {  // sequences before b0 hold `places` places
+  int b0;
+  long long places;
+};
+// The unit that place `x` of the line belongs to, x less than the line's places. Called
+// by the whole CTA with x that never decreases; `shared` and `sums` are in shared memory.
+template <int WARPS>
+__device__ __forceinline__ Part part_at(const AttnParams& p, LineSearch& at, long long x, Part* shared, long long (*sums)[3]) {
+  const int per = p.batch <= 32 ? 32 : WARPS * 32;
+  for (;; at.b0 += per) {
+    const int b = at.b0 + (per == 32 ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x));
+    Units u{0, 1};
+    if (b < p.batch) u = units_of(p, b);
+    const int length = u.tiles + Line::kEnds;
+    const long long own = static_cast<long long>(u.units) * length;
+    long long total = warp_sum(own), end = own;
+    if (total < 1ll << 31) {
+      end = warp_inclusive(static_cast<int>(own));
+    } else {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, end, o);
+        if (static_cast<int>(lane_id()) >= o) end += v;
+      }
+    }
+    if (per > 32) {
+      __syncthreads();  // the previous use of sums and shared is over
+      if (lane_id() == 31) sums[warp_id()][0] = end;
+      __syncthreads();
+      total = 0;
+      for (int w = 0; w < WARPS; ++w) {
+        if (w == static_cast<int>(warp_id())) end += total;
+        total += sums[w][0];
+      }
+    }
+    if (x < at.places + total || at.b0 + per >= p.batch) {
+      const long long i = x - at.places - (end - own);
+      const bool here = i >= 0 && i < own;
+      Part part{b, 0, 0, u.tiles};
+      if (here) {
+        part.unit = own < 1ll << 31 ? static_cast<int>(i) / length : static_cast<int>(i / length);
+        part.place = static_cast<int>(i - static_cast<long long>(part.unit) * length);
+      }
+      if (per == 32) {
+        const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        return {__shfl_sync(0xffffffffu, part.b, from), __shfl_sync(0xffffffffu, part.unit, from),
+                __shfl_sync(0xffffffffu, part.place, from), __shfl_sync(0xffffffffu, part.tiles, from)};
+      }
+      if (here) *shared = part;
+      __syncthreads();
+      return *shared;
+    }
+    at.places += total;
+  }
+}
 
 cudaError_t take_status_attention_prompt(int* status, cudaStream_t st);
 cudaError_t launch_attention_prompt(const AttnParams& p, const AttnMaps& maps, bool bf16, cudaStream_t st);

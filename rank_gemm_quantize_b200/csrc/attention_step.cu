@@ -4,7 +4,8 @@
 //
 // The query heads of a key head and the queries of a sequence form one list of
 // rows (row = query * group + head), cut into tiles of 16. A CTA of four warps
-// takes one item (16 rows, a share of the keys, one key head) after another.
+// takes parts of 16 rows, one key head and some of the keys, one after another: an
+// equal stretch of the call's work (Line).
 // TMA brings 64 keys and values at a time into a ring of stages; each warp
 // takes 16 of them: scores by mma.m16n8k16, softmax statistics and the product
 // with V in registers, with no exchange between warps until the item's end. The
@@ -15,7 +16,7 @@
 // through distributed shared memory.
 //
 // Memory bounds it: 4 dim bytes a key and key head (64 sequences of 200 to 16000
-// keys, 8 key heads of 128, 973 MB: 166 us with the join, 5.9 TB/s, 89% of a copy's
+// keys, 8 key heads of 128, 973 MB: 156 us with the join, 6.2 TB/s, 95% of a copy's
 // rate); 16 rows cost a fraction of the tensor pipe, which is why the narrow mma is
 // used here and a 128-row tensor-memory tile would only add latency. A lone
 // token is latency (777 keys, 4 key heads of 128: 6.1 us on the device; as shares
@@ -91,6 +92,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
   uint64_t* empty = full + L::kStages;
   __shared__ int sums[kWarps][2];
   __shared__ Found found;
+  __shared__ long long line_sums[kWarps][3];
+  __shared__ Part line_part;
   __shared__ int spoiled;
   __shared__ int abort_word;
   __shared__ float warp_ml[kWarps][kStepRows][2];
@@ -111,14 +114,36 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
   __syncthreads();
   if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
+  Line line{};
+  LineSearch along{0, 0};
+  long long x = 0, x_end = 0;  // this CTA's stretch of the line
+  if (!CLUSTER) {
+    line = line_of<kWarps>(p, 0, line_sums);
+    if (static_cast<int>(blockIdx.x) >= line.ctas) return;
+    x = line.begin(blockIdx.x), x_end = line.begin(blockIdx.x + 1);
+  }
   uint32_t used = 0;    // key tiles since the kernel's start
   uint32_t issued = 0;  // ... and how many of them thread 0 has asked for
   Search at{0, 0, 0, p.chunk};
-  for (int item = CLUSTER ? blockIdx.x / kStepCluster : blockIdx.x;; item += gridDim.x) {
-    Found f;
-    if (!find_item<kWarps>(p, at, item, &found, sums, &f)) {  // a cluster's CTAs alike
-      if (CLUSTER) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-      return;
+  for (int item = blockIdx.x / kStepCluster;; item += gridDim.x) {
+    Found f{};
+    Part part{};
+    int first = 0, length = 0;  // key tiles of this part
+    if (CLUSTER) {
+      if (!find_item<kWarps>(p, at, item, &found, sums, &f)) {  // a cluster's CTAs alike
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        return;
+      }
+    } else {
+      if (x >= x_end) return;
+      part = part_at<kWarps>(p, along, x, &line_part, line_sums);
+      const int end = static_cast<int>(min(static_cast<long long>(part.tiles + Line::kEnds), part.place + x_end - x));
+      x += end - part.place;
+      first = max(0, part.place - Line::kEnds);
+      length = end - Line::kEnds - first;
+      if (length <= 0) continue;  // the unit's key tiles are the next CTA's
+      f.b = part.b;
+      f.tile = part.unit;
     }
     int qs, ql, ks, kl;
     seq_extent(p.q_offsets, f.b, p.q_rows, qs, ql);
@@ -137,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
       k_begin = all * share / kStepCluster * kStepKeys;
       k_end = min(all * (share + 1) / kStepCluster * kStepKeys, seen);
     } else {
-      k_begin = f.chunks > 1 ? f.chunk * p.chunk : 0;
-      k_end = min(f.chunks > 1 ? k_begin + p.chunk : kl, seen);
+      k_begin = first * kStepKeys;
+      k_end = min((first + length) * kStepKeys, seen);
     }
     const int first_limit = limit(row0);
     const int tiles = k_end > k_begin ? (k_end - k_begin + kStepKeys - 1) / kStepKeys : 0;
@@ -329,10 +354,10 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
         w[a] = exp2_fast(fmaf(warp_ml[a][r][0], p.scale_log2, -base));
         total = fmaf(warp_ml[a][r][1], w[a], total);
       }
-      const bool split = CLUSTER || f.chunks > 1;
+      const bool split = CLUSTER || length < part.tiles;
       const float norm = split || total == 0.f ? 1.f : 1.f / total;
       const int row_limit = limit(row);
-      const int share = f.slots + f.tile * f.chunks + f.chunk;
+      const int share = 2 * blockIdx.x + (first == 0);
       const size_t slot = (static_cast<size_t>(share) * p.kv_heads + hk) * kStepRows + r;
       const bool fits = share < p.max_slots;
       const int owner = r / L::kOwnRows, slot_row = blockIdx.x % kStepCluster * L::kOwnRows + r % L::kOwnRows;
@@ -422,44 +447,60 @@ __global__ void __launch_bounds__(WIDE * SPLIT * 32) attention_join_kernel(const
   constexpr int kJoinWarps = WIDE * SPLIT;
   __shared__ int sums[kJoinWarps];
   __shared__ Shares own;
+  __shared__ long long line_sums[kJoinWarps][3];
   __shared__ float warp_ml[kJoinWarps][2];
   __shared__ float warp_o[kJoinWarps][DP];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before has ended
   const int b = blockIdx.x, hk = blockIdx.y, warp = warp_id(), lane = lane_id();
-  // the sequence's shares and the slots before its own: up to 32 sequences by the
-  // first warp, since the others have the same to find
-  Shares s{0, 0, 0};
-  int before = 0;
-  if (p.batch > 32 || warp == 0) {
-    const int chunk = key_chunk(p), step = p.batch > 32 ? kJoinWarps * 32 : 32;
-    s = shares_of(p, b, chunk);
-    if (s.slots)
-      for (int j = threadIdx.x; j < b; j += step) before += shares_of(p, j, chunk).slots;
-    before = __reduce_add_sync(0xffffffffu, before);
-  }
-  if (lane == 0) {
-    sums[warp] = before;
-    if (warp == 0) own = s;
-  }
-  __syncthreads();
-  s = own;
-  before = 0;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) before += sums[w];
-  if (!s.slots || before + s.slots > p.max_slots) return;
   int qs, ql;
   seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
+  Shares s{0, 0, 0};
+  int before = 0;
+  Line line{};
+  const int key_tiles = units_of(p, b).tiles;
+  if (WIDE == 1) {
+    if (!ql) return;
+    line = line_of<kJoinWarps>(p, b, line_sums);
+  } else {
+    // the sequence's shares and the slots before its own: up to 32 sequences by the
+    // first warp, since the others have the same to find
+    if (p.batch > 32 || warp == 0) {
+      const int chunk = key_chunk(p), step = p.batch > 32 ? kJoinWarps * 32 : 32;
+      s = shares_of(p, b, chunk);
+      if (s.slots)
+        for (int j = threadIdx.x; j < b; j += step) before += shares_of(p, j, chunk).slots;
+      before = __reduce_add_sync(0xffffffffu, before);
+    }
+    if (lane == 0) {
+      sums[warp] = before;
+      if (warp == 0) own = s;
+    }
+    __syncthreads();
+    s = own;
+    before = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) before += sums[w];
+    if (!s.slots || before + s.slots > p.max_slots) return;
+  }
   constexpr int kPer = DP / 32;
   const int rows = ql * p.group;
   for (int row0 = blockIdx.z * WIDE; row0 < rows; row0 += gridDim.z * WIDE) {
     const int row = min(row0 + warp / SPLIT, rows - 1);
-    const int first = before + row / p.tile_rows * s.chunks, r = row % p.tile_rows;
+    int first = before + row / p.tile_rows * s.chunks, shares = s.chunks;
+    const int r = row % p.tile_rows;
+    if (WIDE == 1) {
+      const long long begin = line.before + static_cast<long long>(row / p.tile_rows) * (key_tiles + Line::kEnds) + Line::kEnds;
+      first = line.cta_of(begin);
+      shares = line.cta_of(begin + key_tiles - 1) - first + 1;
+      if (shares == 1) continue;  // written already
+    }
     float top = -INFINITY, total = 0.f, o[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[e] = 0.f;
 #pragma unroll 4
-    for (int c = warp % SPLIT; c < s.chunks; c += SPLIT) {
-      const size_t slot = (static_cast<size_t>(first + c) * p.kv_heads + hk) * p.tile_rows + r;
+    for (int c = warp % SPLIT; c < shares; c += SPLIT) {
+      const int at = WIDE == 1 ? 2 * (first + c) + (c == 0) : first + c;
+      const size_t slot = (static_cast<size_t>(at) * p.kv_heads + hk) * p.tile_rows + r;
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot);
       float v[kPer];
 #pragma unroll
@@ -518,7 +559,7 @@ cudaError_t start(const AttnParams& p, const AttnMaps& maps, int sms, cudaStream
     return cudaFuncSetAttribute(attention_step_kernel<T, DP, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
   });
   if (e != cudaSuccess) return e;
-  const long long items = p.max_slots + static_cast<long long>(p.q_rows) * p.group / kStepRows + p.batch;
+  const long long items = static_cast<long long>(p.q_rows) * p.group / kStepRows + p.batch;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   cfg.blockDim = dim3(kThreads);
@@ -532,8 +573,7 @@ cudaError_t start(const AttnParams& p, const AttnMaps& maps, int sms, cudaStream
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   } else {
-    // two CTAs an SM go through the items; no more of them than items
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min(items, (2ll * sms + p.kv_heads - 1) / p.kv_heads)), p.kv_heads);
+    cfg.gridDim = dim3(p.ctas, p.kv_heads);
   }
   return cudaLaunchKernelEx(&cfg, attention_step_kernel<T, DP, CLUSTER>, p, maps);
 }
@@ -541,10 +581,10 @@ cudaError_t start(const AttnParams& p, const AttnMaps& maps, int sms, cudaStream
 template <class T, int DP>
 cudaError_t join(const AttnParams& p, cudaStream_t st) {
   // Tiles of many rows have few shares (key_chunk): a warp a row. Of few rows, each has
-  // up to hundreds: four warps a row, or 16 (one token, 250 shares: 18 us with the
-  // shares themselves, 39 with four warps).
+  // up to hundreds: four warps a row, or 16 (one token, 250 shares: 18 us for the
+  // call, 39 with four warps).
   const long long rows = (static_cast<long long>(p.q_rows) * p.group + p.batch - 1) / p.batch;
-  const bool wide = p.tile_rows > kStepRows, many = !wide && p.k_rows / p.chunk > 16 * p.batch;
+  const bool wide = p.tile_rows > kStepRows, many = !wide && p.ctas > 16 * p.batch;
   const int z = static_cast<int>(std::min<long long>(wide ? (rows + 3) / 4 : rows, 4096));
   // set up while the shares are computed; the kernel waits for them itself
   cudaLaunchConfig_t cfg{};
