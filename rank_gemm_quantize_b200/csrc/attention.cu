@@ -74,25 +74,21 @@ svdq_status plan(const svdq_attention_args* c, Plan* out) {
               c->k_rows <= static_cast<long long>(1024) * kStepCluster * c->batch;
   p.prompt = !p.cluster && rows > static_cast<long long>(kStepRows) * c->batch;
   const int key_tile = p.prompt ? kPromptKeys : kStepKeys, tile_rows = p.prompt ? kPromptRows : kStepRows;
-  long long keys, slots = 0;  // keys of a share; partial results
+  long long slots = 0;  // partial results
   if (p.prompt) {
     // where the row tiles alone leave SMs idle, the kernel cuts the keys (key_chunk);
     // its shares are no more than the CTAs that run at once
     const long long tiles = rows / kPromptRows;
     p.fill = p.sms / c->kv_heads;
     p.open = c->batch <= 32 && tiles < p.fill && c->k_rows > 768;  // of fewer keys no share would have 512
-    keys = c->k_rows;
     slots = p.open ? p.fill : 0;
-  } else if (p.cluster) {
-    keys = c->k_rows;
-  } else {
+  } else if (!p.cluster) {
     // two CTAs an SM, no more than there are stretches (Line) that are worth one
     const long long units = rows / kStepRows + c->batch;
     p.ctas = static_cast<int>(std::min(std::max(1ll, 2ll * p.sms / c->kv_heads), units + c->k_rows / (Line::kLeast * kStepKeys)));
-    keys = c->k_rows;
     slots = 2ll * p.ctas;
   }
-  p.chunk = static_cast<int>(std::max<long long>(1, (keys + key_tile - 1) / key_tile) * key_tile);
+  p.chunk = std::max(1, (c->k_rows + key_tile - 1) / key_tile) * key_tile;
   if ((slots + rows / tile_rows + c->batch) * c->kv_heads > 0x7fffffffll) return fail(SVDQ_ERR_UNSUPPORTED, "too many sequences times heads");
   p.max_slots = static_cast<int>(slots);
   const size_t slot_rows = static_cast<size_t>(slots) * c->kv_heads * tile_rows;
@@ -170,7 +166,7 @@ svdq_status svdq_attention_forward(const svdq_attention_args* a, void* stream) {
     return fail(SVDQ_ERR_CUDA, "cuTensorMapEncodeTiled (keys or values) failed");
   const bool bf16 = a->dtype == SVDQ_BF16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = pl.prompt ? launch_attention_prompt(p, maps, bf16, st) : launch_attention_step(p, maps, bf16, pl.cluster, pl.sms, st);
+  cudaError_t e = pl.prompt ? launch_attention_prompt(p, maps, bf16, st) : launch_attention_step(p, maps, bf16, pl.cluster, st);
   if (e == cudaSuccess && pl.max_slots > 0) e = launch_attention_join(p, bf16, st);
   if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("attention kernel: ") + cudaGetErrorString(e));
   return SVDQ_OK;

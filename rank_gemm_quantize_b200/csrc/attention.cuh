@@ -361,6 +361,6 @@ cudaError_t launch_attention_prompt(const AttnParams& p, const AttnMaps& maps, b
 // Joins the shares of the sequences that have several (after either kernel).
 cudaError_t launch_attention_join(const AttnParams& p, bool bf16, cudaStream_t st);
 cudaError_t take_status_attention_step(int* status, cudaStream_t st);
-cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, bool cluster, int sms, cudaStream_t st);
+cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, bool cluster, cudaStream_t st);
 
 }  // namespace svdq

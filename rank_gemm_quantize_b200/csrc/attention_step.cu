@@ -8,9 +8,9 @@
 // equal stretch of the call's work (Line).
 // TMA brings 64 keys and values at a time into a ring of stages; each warp
 // takes 16 of them: scores by mma.m16n8k16, softmax statistics and the product
-// with V in registers, with no exchange between warps until the item's end. The
-// shares' results (unnormalised float sums, maximum, sum) go to the workspace,
-// or straight to the output where a sequence has one share. A call of so few and
+// with V in registers, with no exchange between warps until the part's end. The
+// parts' results (unnormalised float sums, maximum, sum) go to the workspace, or
+// straight to the output where a row tile is one part. A call of so few and
 // short sequences that eight CTAs an item are all there is to gain takes one
 // launch: the eight are a cluster, cut the keys evenly and join their results
 // through distributed shared memory.
@@ -552,20 +552,20 @@ __global__ void __launch_bounds__(WIDE * SPLIT * 32) attention_join_kernel(const
 }
 
 template <class T, int DP, bool CLUSTER>
-cudaError_t start(const AttnParams& p, const AttnMaps& maps, int sms, cudaStream_t st) {
+cudaError_t start(const AttnParams& p, const AttnMaps& maps, cudaStream_t st) {
   using L = StepSmem<DP>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = once_per_device(done, [] {
     return cudaFuncSetAttribute(attention_step_kernel<T, DP, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
   });
   if (e != cudaSuccess) return e;
-  const long long items = static_cast<long long>(p.q_rows) * p.group / kStepRows + p.batch;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::kTotal;
   cfg.stream = st;
   if (CLUSTER) {
+    const long long items = static_cast<long long>(p.q_rows) * p.group / kStepRows + p.batch;
     cfg.gridDim = dim3(static_cast<unsigned>(items) * kStepCluster, p.kv_heads);
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kStepCluster;
@@ -608,13 +608,13 @@ namespace svdq {
 cudaError_t take_status_attention_step(int* status, cudaStream_t st) { return take_status(status, st); }
 
 template <class T>
-static cudaError_t start_dim(const AttnParams& p, const AttnMaps& maps, bool cluster, int sms, cudaStream_t st) {
-  if (p.dim <= 64) return cluster ? start<T, 64, true>(p, maps, sms, st) : start<T, 64, false>(p, maps, sms, st);
-  return cluster ? start<T, 128, true>(p, maps, sms, st) : start<T, 128, false>(p, maps, sms, st);
+static cudaError_t start_dim(const AttnParams& p, const AttnMaps& maps, bool cluster, cudaStream_t st) {
+  if (p.dim <= 64) return cluster ? start<T, 64, true>(p, maps, st) : start<T, 64, false>(p, maps, st);
+  return cluster ? start<T, 128, true>(p, maps, st) : start<T, 128, false>(p, maps, st);
 }
 
-cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, bool cluster, int sms, cudaStream_t st) {
-  return bf16 ? start_dim<__nv_bfloat16>(p, maps, cluster, sms, st) : start_dim<__half>(p, maps, cluster, sms, st);
+cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, bool cluster, cudaStream_t st) {
+  return bf16 ? start_dim<__nv_bfloat16>(p, maps, cluster, st) : start_dim<__half>(p, maps, cluster, st);
 }
 
 cudaError_t launch_attention_join(const AttnParams& p, bool bf16, cudaStream_t st) {
