@@ -349,3 +349,20 @@ def test_shares_and_join_in_a_graph(q_lengths, k_lengths):
         torch.cuda.synchronize()
         ops.check(o, *ops.attention(q, k, v, q_lengths, k2, True))
     assert rq.operator_status() == rq.Status.OK
+
+
+# One odd key, at another of the 32 places of a block of scores for each of 32 heads: prompts, shares of the
+# keys and their join, single tokens by stretches and by clusters.
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("q_lengths,k_lengths,first,causal", [
+    ([40, 40], [200, 90], 32, False), ([200], [200], 0, True), ([200], [200], 96, True), ([40], [3000], 1056, False),
+    ([40], [3000], 2944, True), ([1, 1, 1], [700, 30, 5], 640, True), ([1], [777], 64, True)])
+@pytest.mark.parametrize("dim,dtype", [(64, F16), (128, BF16)])
+def test_one_odd_key_at_every_place(q_lengths, k_lengths, first, causal, dim, dtype, value):
+    """A NaN or an infinity among the scores that a row sees makes the row NaN."""
+    q, k, v = make(41, q_lengths, k_lengths, 32, 32, dim, dtype)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    for h in range(32):
+        k[first + h, h, 0] = value
+    o = run(q, k, v, q_lengths, k_lengths, causal)
+    ops.check(o, *ops.attention(q, k, v, q_lengths, k_lengths, causal))
