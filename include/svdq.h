@@ -348,7 +348,8 @@ typedef enum {
  * over the keys j of the query's own sequence; with `causal`, query i of Lq
  * sees keys j <= i + Lk - Lq (the last query sees every key, so a sequence's
  * queries may be a whole prompt, a piece of one, or a single new token against
- * all the keys so far). A query that sees no key gives 0. Keys a query does not
+ * all the keys so far). A query that sees no key gives 0; one that sees only
+ * scores of minus infinity gives NaN, as the formula does. Keys a query does not
  * see never reach its result, whatever they hold (infinities and NaN
  * included). Query head h reads key head h / (q_heads / kv_heads).
  * Scores, softmax statistics and sums are float; the probabilities are rounded

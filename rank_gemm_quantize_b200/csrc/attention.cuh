@@ -91,6 +91,20 @@ __device__ __forceinline__ void store_shared(uint32_t addr, uint32_t a, uint32_t
 }
 __device__ __forceinline__ void store_shared(uint32_t addr, const uint4& v) { store_shared(addr, v.x, v.y, v.z, v.w); }
 
+// The last key that a row (query * group + head) of a sequence of ql queries and kl keys
+// sees, below 0 if it sees none.
+__device__ __forceinline__ int last_key(const AttnParams& p, int row, int ql, int kl) {
+  return p.causal ? min(row / p.group + kl - ql, kl - 1) : kl - 1;
+}
+// What a row's products with V are multiplied by. A sum of 0: the row sees no key (last()
+// is below 0) and its result is 0, or every key that it sees has a score of minus
+// infinity, and its result is NaN.
+template <class Last>
+__device__ __forceinline__ float row_norm(float sum, Last last) {
+  if (sum == 0.f) return last() < 0 ? 1.f : __uint_as_float(0x7FFFFFFFu);
+  return 1.f / sum;
+}
+
 // 2^x in one instruction (results under the normal range become 0).
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;

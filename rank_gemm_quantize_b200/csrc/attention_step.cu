@@ -152,8 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
     const int row0 = f.tile * kStepRows;
     // keys [k_begin, k_end) of this share; row r sees keys <= limit(r)
     auto limit = [&](int row) {
-      if (row >= rows) return -1;
-      return p.causal ? min(row / p.group + kl - ql, kl - 1) : kl - 1;
+      return row < rows ? last_key(p, row, ql, kl) : -1;
     };
     const int seen = limit(min(row0 + kStepRows, rows) - 1) + 1;  // keys that some row sees
     int k_begin, k_end;
@@ -355,8 +354,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
         total = fmaf(warp_ml[a][r][1], w[a], total);
       }
       const bool split = CLUSTER || length < part.tiles;
-      const float norm = split || total == 0.f ? 1.f : 1.f / total;
       const int row_limit = limit(row);
+      const float norm = split ? 1.f : row_norm(total, [&] { return row_limit; });
       const int share = 2 * blockIdx.x + (first == 0);
       const size_t slot = (static_cast<size_t>(share) * p.kv_heads + hk) * kStepRows + r;
       const bool fits = share < p.max_slots;
@@ -425,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
           for (int e = 0; e < kCols; ++e)
             o[e] = fmaf(reinterpret_cast<const float*>(smem + L::kSums)[(s * L::kOwnRows + own) * L::kPitch + c + e], w, o[e]);
         }
-        const float norm = total == 0.f ? 1.f : 1.f / total;
+        const float norm = row_norm(total, [&] { return limit(mine); });
         T* out = static_cast<T*>(p.out) + (static_cast<size_t>(qs + mine / p.group) * p.q_heads + hk * p.group + mine % p.group) * p.dim + c;
         if constexpr (kCols == 2)
           *reinterpret_cast<uint32_t*>(out) = Half16<T>::pack(o[0] * norm, o[1] * norm);
@@ -540,7 +539,11 @@ __global__ void __launch_bounds__(WIDE * SPLIT * 32) attention_join_kernel(const
     } else if (row0 + warp >= rows) {
       continue;
     }
-    const float norm = total == 0.f ? 1.f : 1.f / total;
+    const float norm = row_norm(total, [&] {
+      int start, kl;
+      seq_extent(p.k_offsets, b, p.k_rows, start, kl);
+      return last_key(p, row, ql, kl);
+    });
     if (kPer * lane < p.dim) {
       T* out = static_cast<T*>(p.out) + (static_cast<size_t>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim + kPer * lane;
       if constexpr (kPer == 4)

@@ -366,3 +366,23 @@ def test_one_odd_key_at_every_place(q_lengths, k_lengths, first, causal, dim, dt
         k[first + h, h, 0] = value
     o = run(q, k, v, q_lengths, k_lengths, causal)
     ops.check(o, *ops.attention(q, k, v, q_lengths, k_lengths, causal))
+
+
+@pytest.mark.parametrize("every", [False, True])
+@pytest.mark.parametrize("q_lengths,k_lengths,kv_heads", [
+    ([40, 3], [200, 90], 32), ([200], [150], 32), ([40], [3000], 32), ([1500], [1300], 2), ([1, 1, 1], [700, 30, 5], 32),
+    ([12, 1], [9, 3000], 32), ([1], [777], 32), ([9], [5], 2)])
+@pytest.mark.parametrize("dim,dtype", [(64, F16), (128, BF16)])
+def test_scores_of_minus_infinity(q_lengths, k_lengths, kv_heads, dim, dtype, every):
+    """Minus infinity leaves a key out; a row that sees only such keys is NaN, one that sees no key at all is 0."""
+    q, k, v = make(42, q_lengths, k_lengths, kv_heads, kv_heads, dim, dtype)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    if every:
+        k[:k_lengths[0], :, 0] = float("-inf")
+    else:
+        for h in range(kv_heads):
+            k[h % k_lengths[0], h, 0] = float("-inf")
+    o = run(q, k, v, q_lengths, k_lengths, True)
+    want, bound = ops.attention(q, k, v, q_lengths, k_lengths, True)
+    assert want.isnan().any() or not every
+    ops.check(o, want, bound)
