@@ -526,9 +526,12 @@ def _call_stream(device: int, stream, *made: torch.Tensor) -> int:
         return current
     handle = _stream(stream)
     if handle != current:
+        if not isinstance(stream, torch.cuda.Stream):
+            # torch takes handle 0 for none given: an ExternalStream of it would be a stream of torch's pool
+            stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
         for t in made:
             if t is not None:
-                t.record_stream(torch.cuda.ExternalStream(handle, device))
+                t.record_stream(stream)
     return handle
 
 
