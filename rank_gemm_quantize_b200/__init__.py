@@ -519,20 +519,36 @@ def _offsets(name: str, t: torch.Tensor, device: int):
     return t.data_ptr(), n - 1
 
 
-def _call_stream(device: int, stream, *made: torch.Tensor) -> int:
-    """The stream of a call; what the call allocated stays valid for it."""
-    current = _raw_stream(device)
-    if stream is None:
-        return current
+def _other_stream(device: int, stream):
+    """The torch stream of a call's `stream`, or None where it is the current one."""
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
+        return None if stream.cuda_stream == _raw_stream(device) else stream
     handle = _stream(stream)
-    if handle != current:
-        if not isinstance(stream, torch.cuda.Stream):
-            # torch takes handle 0 for none given: an ExternalStream of it would be a stream of torch's pool
-            stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
-    return handle
+    if handle == _raw_stream(device):
+        return None
+    # torch takes handle 0 for none given: an ExternalStream of it would be a stream of torch's pool
+    return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+
+
+def _on_stream(device: int, other, call, *args, **names):
+    """The call with stream `other` as the current one.
+
+    What it makes is allocated there: memory that the caller's stream has freed
+    may still be in use on that stream. Results may be used and dropped on the
+    caller's stream."""
+    caller = torch.cuda.current_stream(device)
+    torch.cuda.set_stream(other)  # of the current device; torch.cuda.stream() takes 6 us more
+    try:
+        results = call(*args, **names)
+    finally:
+        torch.cuda.set_stream(caller)
+    given = [t for t in (*args, *names.values()) if isinstance(t, torch.Tensor)]
+    for t in results if isinstance(results, tuple) else (results,):
+        if t is not None and not any(t is g for g in given):
+            t.record_stream(caller)
+    return results
 
 
 def _attention_shapes(q, k, v, batch):
@@ -579,11 +595,15 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opti
     without either all rows are one sequence). causal: the last query of a
     sequence sees every key, the one before it all but one, and so on. scale
     defaults to dim ** -0.5. Rows of `out` that belong to no sequence are not
-    written."""
+    written. stream: the call runs on it, behind what is queued there; the
+    caller orders it after the work that makes the inputs and before the work
+    that uses the result."""
     device = _place(q)
     if device != _current_device():
         with torch.cuda.device(device):
             return attention(q, k, v, q_offsets, k_offsets, causal, scale, out, workspace, stream)
+    if stream is not None and (other := _other_stream(device, stream)) is not None:
+        return _on_stream(device, other, attention, q, k, v, q_offsets, k_offsets, causal, scale, out, workspace)
     batch, qo, ko = 1, 0, 0
     if q_offsets is not None:
         qo, batch = _offsets("q_offsets", q_offsets, device)
@@ -601,9 +621,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opti
     (qr, qh, q1), (kr, kh, k1), (vr, vh, v1) = q.stride(), k.stride(), v.stride()
     if q1 != 1 or k1 != 1 or v1 != 1:
         raise ValueError("the values of a head of q, k and v must be contiguous")
-    made_out = made_workspace = None
     if out is None:
-        out = made_out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(tuple(q.shape))
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(tuple(q.shape))
         o = out.data_ptr()
     else:
         o = _operand("out", out, q.dtype, device, q.shape)
@@ -613,11 +632,11 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opti
             raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
         ws, need = workspace.data_ptr(), workspace.numel()
     elif need:
-        made_workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws = made_workspace.data_ptr()
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = workspace.data_ptr()
     args = _pack_attention(*shapes, 1 if causal else 0, shapes[6] ** -0.5 if scale is None else scale, qr, qh, kr, kh, vr, vh,
                            q.data_ptr(), k.data_ptr(), v.data_ptr(), qo, ko, o, ws, need)
-    _check(lib().svdq_attention_forward(args, _call_stream(device, stream, made_out, made_workspace)))
+    _check(lib().svdq_attention_forward(args, _raw_stream(device)))
     return out
 
 
@@ -626,7 +645,7 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     """residual + activation(X W + bias) for a layer whose weight stays in 16 bits
     (include/svdq.h, svdq_dense_linear_forward): X [M, K], W [K, N], bias [N],
     residual and out [M, N], all bfloat16 or all float16; activation None, "relu",
-    "silu", "gelu" or "gelu_tanh". out may be the residual."""
+    "silu", "gelu" or "gelu_tanh". out may be the residual. stream as in attention()."""
     dtype = X.dtype
     if X.dim() != 2 or W.dim() != 2 or dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("X and W must be bfloat16 or float16 matrices")
@@ -637,20 +656,21 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     if device != _current_device():
         with torch.cuda.device(device):
             return linear(X, W, bias, activation, residual, out, stream)
+    if stream is not None and (other := _other_stream(device, stream)) is not None:
+        return _on_stream(device, other, linear, X, W, bias, activation, residual, out)
     (M, K), N = X.shape, W.shape[1]
     if not X.is_contiguous():
         raise ValueError("X must be contiguous")
     w = _operand("W", W, dtype, device, (K, N))
     b = 0 if bias is None else _operand("bias", bias, dtype, device, (N,))
     r = 0 if residual is None else _operand("residual", residual, dtype, device, (M, N))
-    made = None
     if out is None:
-        out = made = X.new_empty((M, N)) if residual is None else torch.empty_like(residual)
+        out = X.new_empty((M, N)) if residual is None else torch.empty_like(residual)
         y = out.data_ptr()
     else:
         y = _operand("out", out, dtype, device, (M, N))
     args = _pack_dense_linear(_DTYPE[dtype], act, M, K, N, X.data_ptr(), w, b, r, y)
-    _check(lib().svdq_dense_linear_forward(args, _call_stream(device, stream, made)))
+    _check(lib().svdq_dense_linear_forward(args, _raw_stream(device)))
     return out
 
 
@@ -673,7 +693,8 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
     offsets[b] to offsets[b + 1] (without offsets, one row for all). Without y
     (the first norm of a model) x' is x itself and only h is computed, in `dtype`
     (that of x where x is not float32); with norm None h is None. out_x may be x,
-    out_h may be y. Rows that belong to no sequence are not written."""
+    out_h may be y. Rows that belong to no sequence are not written. stream as in
+    attention()."""
     x_kind = x.dtype
     if x.dim() != 2 or x_kind not in _DTYPE:
         raise ValueError("x must be a [rows, dim] tensor of bfloat16, float16 or float32")
@@ -690,11 +711,15 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
             return residual_norm(x, y, offsets=offsets, gate=gate, residual_scale=residual_scale, post_norm=post_norm,
                                  post_weight=post_weight, post_bias=post_bias, norm=norm, weight=weight, bias=bias,
                                  scale=scale, shift=shift, eps=eps, dtype=dtype, out_x=out_x, out_h=out_h, stream=stream)
+    if stream is not None and (other := _other_stream(device, stream)) is not None:
+        return _on_stream(device, other, residual_norm, x, y, offsets=offsets, gate=gate, residual_scale=residual_scale,
+                          post_norm=post_norm, post_weight=post_weight, post_bias=post_bias, norm=norm, weight=weight,
+                          bias=bias, scale=scale, shift=shift, eps=eps, dtype=dtype, out_x=out_x, out_h=out_h)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     shape = x.shape
     rows, dim = shape
-    seqs, off, made_x, made_h, x_out, h_out = 1, None, None, None, 0, 0
+    seqs, off, x_out, h_out = 1, None, 0, 0
     if offsets is not None:
         off, seqs = _offsets("offsets", offsets, device)
     of_row, of_seq = (dim,), (seqs, dim)
@@ -702,7 +727,7 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
         gate, scale, shift = (None if t is None else t.view(1, -1) if t.dim() == 1 else t for t in (gate, scale, shift))
     if y is not None:
         if out_x is None:
-            out_x = made_x = torch.empty_like(x)
+            out_x = torch.empty_like(x)
             x_out = out_x.data_ptr()
         else:
             x_out = _operand("out_x", out_x, x_kind, device, shape)
@@ -710,7 +735,7 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
         raise ValueError("without y there is no out_x")
     if norm is not None:
         if out_h is None:
-            out_h = made_h = torch.empty_like(x, dtype=kind) if y is None else torch.empty_like(y)
+            out_h = torch.empty_like(x, dtype=kind) if y is None else torch.empty_like(y)
             h_out = out_h.data_ptr()
         else:
             h_out = _operand("out_h", out_h, kind, device, shape)
@@ -726,7 +751,7 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
         0 if bias is None else _operand("bias", bias, kind, device, of_row),
         0 if scale is None else _operand("scale", scale, kind, device, of_seq),
         0 if shift is None else _operand("shift", shift, kind, device, of_seq), off or 0)
-    _check(lib().svdq_residual_norm(args, _call_stream(device, stream, made_x, made_h)))
+    _check(lib().svdq_residual_norm(args, _raw_stream(device)))
     return x if y is None else out_x, out_h
 
 

@@ -61,6 +61,23 @@ def filled(nbytes):
     return [torch.full((nbytes,), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
 
 
+def test_memory_that_the_current_stream_still_reads(case):
+    """Work under way on the current stream reads a temporary that is freed before the call on another stream."""
+    call, inputs, want, nbytes = case
+    side = torch.cuda.Stream()
+    temporary = filled(nbytes)
+    read = [torch.empty_like(t) for t in temporary]
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(LONG)
+    for r, t in zip(read, temporary):
+        r.copy_(t)
+    del temporary, r, t
+    got = call(inputs, side)
+    torch.cuda.synchronize()
+    assert all((r == 7).all() for r in read)
+    right(got, want)
+
+
 @pytest.mark.parametrize("handle", [False, True])
 def test_the_default_stream_under_another_current_one(case, handle):
     """What a call on the default stream makes and drops is not handed to the current stream while the call waits."""
@@ -74,3 +91,36 @@ def test_the_default_stream_under_another_current_one(case, handle):
     torch.cuda.synchronize()
     assert all((t == 7).all() for t in later)
     right(got, want)
+
+
+def test_results_used_on_the_current_stream_and_dropped(case):
+    """The next tensors of the call's stream do not lie where the current stream still reads a result."""
+    call, inputs, want, nbytes = case
+    side = torch.cuda.Stream()
+    got = call(inputs, side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(LONG)
+    read = [t.clone() for t in got]
+    del got
+    with torch.cuda.stream(side):
+        over = [torch.full_like(t, 7.0) for t in read]
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in over)
+    right(read, want)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_captured_on_a_joined_stream(case, raw):
+    """A call on a second stream of a capture, replayed."""
+    call, inputs, want, _ = case
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(inputs, side.cuda_stream if raw else side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        right(got, want)
