@@ -537,7 +537,7 @@ def _on_stream(device: int, other, call, *args, **names):
 
     What it makes is allocated there: memory that the caller's stream has freed
     may still be in use on that stream. Results may be used and dropped on the
-    caller's stream."""
+    caller's stream, and what was given may be dropped after the call."""
     caller = torch.cuda.current_stream(device)
     torch.cuda.set_stream(other)  # of the current device; torch.cuda.stream() takes 6 us more
     try:
@@ -545,6 +545,8 @@ def _on_stream(device: int, other, call, *args, **names):
     finally:
         torch.cuda.set_stream(caller)
     given = [t for t in (*args, *names.values()) if isinstance(t, torch.Tensor)]
+    for t in given:
+        t.record_stream(other)
     for t in results if isinstance(results, tuple) else (results,):
         if t is not None and not any(t is g for g in given):
             t.record_stream(caller)

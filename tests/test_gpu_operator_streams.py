@@ -109,6 +109,20 @@ def test_results_used_on_the_current_stream_and_dropped(case):
     right(read, want)
 
 
+def test_inputs_dropped_after_the_call(case):
+    """The next tensors of the current stream do not lie where the call still reads its inputs."""
+    call, inputs, want, _ = case
+    side = torch.cuda.Stream()
+    sizes = [t.nbytes for t in inputs]
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(LONG)
+    got = call([t.clone() for t in inputs], side)  # the clones come long before the call runs
+    over = [torch.full((n,), 0, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    del over
+    right(got, want)
+
+
 @pytest.mark.parametrize("raw", [False, True])
 def test_captured_on_a_joined_stream(case, raw):
     """A call on a second stream of a capture, replayed."""
