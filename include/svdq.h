@@ -457,6 +457,13 @@ SVDQ_API void svdq_debug_fail_allocation(long long index);
  * context stays usable). Synchronizes `stream`. */
 SVDQ_API svdq_status svdq_selftest_bounded_wait(unsigned long long limit_ns, void* stream);
 
+/* As above for the words that svdq_operator_status reads: launches, among the
+ * kernels of attention of few queries (0), of many (1) or of the 16-bit linear
+ * layer (2), one in which a lane waits in vain with the library's own limit (about
+ * two seconds). Its warp gives up together, and the next svdq_operator_status
+ * returns SVDQ_ERR_DEVICE_TIMEOUT. */
+SVDQ_API svdq_status svdq_selftest_operator_wait(int kernels, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

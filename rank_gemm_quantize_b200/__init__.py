@@ -132,6 +132,7 @@ SIGNATURES = {
     "svdq_dense_linear_forward": [_VP, _VP],
     "svdq_residual_norm": [_VP, _VP],
     "svdq_operator_status": [_VP],
+    "svdq_selftest_operator_wait": [_I, _VP],
 }
 
 
@@ -755,6 +756,11 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, offsets:
         0 if shift is None else _operand("shift", shift, kind, device, of_seq), off or 0)
     _check(lib().svdq_residual_norm(args, _raw_stream(device)))
     return x if y is None else out_x, out_h
+
+
+def selftest_operator_wait(kernels: int, stream=None) -> None:
+    """A wait in vain that operator_status() then reports (include/svdq.h, svdq_selftest_operator_wait)."""
+    _check(lib().svdq_selftest_operator_wait(kernels, _stream(stream)))
 
 
 def operator_status(stream=None) -> Status:

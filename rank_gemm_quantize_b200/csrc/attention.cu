@@ -8,6 +8,7 @@
 namespace svdq {
 void set_last_error(const std::string& msg);
 cudaError_t take_status_dense(int* status, cudaStream_t st);
+cudaError_t give_up_dense(cudaStream_t st);
 }  // namespace svdq
 
 using namespace svdq;
@@ -182,6 +183,14 @@ svdq_status svdq_operator_status(void* stream) {
     timeout |= status == kDevTimeout;
   }
   if (timeout) return fail(SVDQ_ERR_DEVICE_TIMEOUT, "a kernel gave up a pipeline wait");
+  return SVDQ_OK;
+}
+
+svdq_status svdq_selftest_operator_wait(int kernels, void* stream) {
+  constexpr cudaError_t (*start[])(cudaStream_t) = {give_up_attention_step, give_up_attention_prompt, give_up_dense};
+  if (kernels < 0 || kernels > 2) return fail(SVDQ_ERR_INVALID_ARG, "kernels must be 0, 1 or 2");
+  const cudaError_t e = start[kernels](static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("self-test kernel: ") + cudaGetErrorString(e));
   return SVDQ_OK;
 }
 

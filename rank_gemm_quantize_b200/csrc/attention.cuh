@@ -371,10 +371,12 @@ __device__ __forceinline__ Part part_at(const AttnParams& p, LineSearch& at, lon
 }
 
 cudaError_t take_status_attention_prompt(int* status, cudaStream_t st);
+cudaError_t give_up_attention_prompt(cudaStream_t st);
 cudaError_t launch_attention_prompt(const AttnParams& p, const AttnMaps& maps, bool bf16, cudaStream_t st);
 // Joins the shares of the sequences that have several (after either kernel).
 cudaError_t launch_attention_join(const AttnParams& p, bool bf16, cudaStream_t st);
 cudaError_t take_status_attention_step(int* status, cudaStream_t st);
+cudaError_t give_up_attention_step(cudaStream_t st);
 cudaError_t launch_attention_step(const AttnParams& p, const AttnMaps& maps, bool bf16, bool cluster, cudaStream_t st);
 
 }  // namespace svdq

@@ -98,12 +98,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A wait of a whole warp. No lane goes ahead before all are through: one that fell
-// behind by two phases would take the wrong one for its own; and all give up, or none.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
-}
-
 // 2^x of two values without the exponential unit: x = i + f, f in [-1/2, 1/2]; the
 // polynomial (minimax in the relative error by Lawson's iteration, 2.6e-6) gives
 // 2^f, and i goes into its exponent. 0 below 2^-126, as a hidden key needs. Of NaN it
@@ -583,6 +577,7 @@ cudaError_t start(const AttnParams& p, const AttnMaps& maps, cudaStream_t st) {
 namespace svdq {
 
 cudaError_t take_status_attention_prompt(int* status, cudaStream_t st) { return take_status(status, st); }
+cudaError_t give_up_attention_prompt(cudaStream_t st) { return give_up(st); }
 
 cudaError_t launch_attention_prompt(const AttnParams& p, const AttnMaps& maps, bool bf16, cudaStream_t st) {
   if (p.dim <= 64) return bf16 ? start<__nv_bfloat16, 64>(p, maps, st) : start<__half, 64>(p, maps, st);

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
     for (; i < tiles; ++i) {
       const uint32_t n = used + i;
       const int s = n % L::kStages;
-      if (!mbar_wait(&full[s], (n / L::kStages) & 1, abort_flag, &g_status)) break;
+      if (!warp_wait(&full[s], (n / L::kStages) & 1, abort_flag, &g_status)) break;
       uint8_t* st = smem + s * L::kStage;
       const uint32_t kt = smem_u32(st), vt = kt + L::kTile;
       const int key0 = k_begin + i * kStepKeys + 16 * warp;  // the warp's 16 keys
@@ -609,6 +609,7 @@ cudaError_t join(const AttnParams& p, cudaStream_t st) {
 namespace svdq {
 
 cudaError_t take_status_attention_step(int* status, cudaStream_t st) { return take_status(status, st); }
+cudaError_t give_up_attention_step(cudaStream_t st) { return give_up(st); }
 
 template <class T>
 static cudaError_t start_dim(const AttnParams& p, const AttnMaps& maps, bool cluster, cudaStream_t st) {

@@ -123,6 +123,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// A wait of a whole warp. No lane goes ahead before all are through: one that fell
+// behind by two phases would take the wrong one for its own. And all give up, or
+// none: what follows may be an instruction of the whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
+
 // As mbar_wait, for a barrier that other CTAs of the cluster arrive on after
 // plain stores to this CTA's shared memory: the stores are visible afterwards.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {

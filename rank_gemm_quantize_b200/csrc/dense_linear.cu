@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DensePar
   };
   uint4 res = residual(r0);
   volatile int no_abort = 0;
-  mbar_wait(acc_full, 0, &no_abort, &g_status);
+  warp_wait(acc_full, 0, &no_abort, &g_status);
   tc_fence_after();
 
   // The partial sums go to the owners of the rows, [share][row of the slice][column];
@@ -465,10 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const uint32_t idesc = idesc_dense(kFmtF32, Half16<T>::kFmt, Half16<T>::kFmt, kPairM, NT) | (1u << 16);
       const bool issues = elect_one();
       const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0), ring = smem_u32(smem);
-      // all lanes or none: no lane falls behind by two phases
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &g_status)) != 0;
-      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, abort_flag, &g_status); };
       bool ok = true;
       uint32_t it = 0;
       int ti = 0;
@@ -527,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       };
       fetch(0);
-      if (!mbar_wait(&acc_full[buf], (ti >> 1) & 1, abort_flag, &g_status)) break;
+      if (!warp_wait(&acc_full[buf], (ti >> 1) & 1, abort_flag, &g_status)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < NT / 2; c += 32) {
@@ -585,8 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   if (warp == 1) {
     volatile int no_abort = 0;
-    mbar_wait(drain, 0, &no_abort, nullptr);
-    __syncwarp();
+    warp_wait(drain, 0, &no_abort, nullptr);
   }
   tc_fence_before();
   if (*abort_flag) asm volatile("fence.acq_rel.cluster;" ::: "memory");
@@ -640,6 +636,7 @@ svdq_status run(const DenseParams& p, const void* X, const void* W, cudaStream_t
 
 namespace svdq {
 cudaError_t take_status_dense(int* status, cudaStream_t st) { return take_status(status, st); }
+cudaError_t give_up_dense(cudaStream_t st) { return give_up(st); }
 }  // namespace svdq
 
 extern "C" svdq_status svdq_dense_linear_forward(const svdq_dense_linear_args* a, void* stream) {

@@ -19,4 +19,27 @@ static cudaError_t take_status(int* status, cudaStream_t st) {
   return e;
 }
 
+// Self-test: one lane waits for an arrival that never comes, the others for one that
+// has. All of them have to give up; a lane that went on would clear the word again.
+static __global__ void give_up_kernel() {
+  __shared__ uint64_t bars[2];
+  __shared__ int abort_word;
+  if (threadIdx.x == 0) {
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    abort_word = 0;
+    fence_barrier_init();
+    mbar_arrive(&bars[1]);
+  }
+  __syncthreads();
+  const bool ok = warp_wait(&bars[lane_id() > 0], 0, &abort_word, &g_status);
+  __syncwarp();
+  if (ok) atomicExch(&g_status, kDevOk);
+}
+
+static cudaError_t give_up(cudaStream_t st) {
+  give_up_kernel<<<1, 32, 0, st>>>();
+  return cudaGetLastError();
+}
+
 }  // namespace svdq

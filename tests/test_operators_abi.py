@@ -130,3 +130,8 @@ def test_binding_refuses_unknown_names(rq):
         rq.residual_norm(t.double())
     with pytest.raises(ValueError, match="bfloat16 or float16"):
         rq.linear(t.float(), t.float())
+
+
+@pytest.mark.parametrize("kernels", [-1, 3])
+def test_selftest_refuses_unknown_kernels(rq, kernels):
+    refused(rq, rq.lib().svdq_selftest_operator_wait(kernels, None), INVALID, b"kernels")
