@@ -179,16 +179,16 @@ struct Found {
   int b, tile, tiles, chunk, chunks;
   int slots;  // workspace slots before the sequence's; it has slot tile * chunks + chunk of its own
 };
-struct Search {  // where the search for an item stands: sequences before b0 hold `items` items and `slots` slots
-  int b0, items, slots;
+struct Search {  // where the search for an item stands: sequences before b0 hold `items` items
+  int b0, items;
   int chunk;  // key_chunk
 };
 
 // The sequence, row tile and key share of item `idx`: false behind the last.
 // Called by the whole CTA of WARPS warps with idx that never decreases; `shared`
-// and `sums` are in shared memory.
+// and `sums` are in shared memory. The keys of more than 32 sequences are not cut.
 template <int WARPS>
-__device__ bool find_item(const AttnParams& p, Search& at, int idx, Found* shared, int (*sums)[2], Found* found) {
+__device__ bool find_item(const AttnParams& p, Search& at, int idx, Found* shared, int* sums, Found* found) {
   if (p.batch <= 32) {  // each warp for itself, no barrier
     const int lane = lane_id();
     Shares s{0, 0, 0};
@@ -207,40 +207,25 @@ __device__ bool find_item(const AttnParams& p, Search& at, int idx, Found* share
   }
   for (; at.b0 < p.batch; at.b0 += WARPS * 32) {
     const int b = at.b0 + static_cast<int>(threadIdx.x);
-    Shares s{0, 0, 0};
-    if (b < p.batch) s = shares_of(p, b, at.chunk);
-    const int own = s.tiles * s.chunks;
-    int items = warp_inclusive(own), slots = warp_inclusive(s.slots);
+    const int own = b < p.batch ? shares_of(p, b, at.chunk).tiles : 0;
+    int items = warp_inclusive(own);
     __syncthreads();  // the previous use of sums and found is over
-    if (lane_id() == 31) {
-      sums[warp_id()][0] = items;
-      sums[warp_id()][1] = slots;
-    }
+    if (lane_id() == 31) sums[warp_id()] = items;
     __syncthreads();
-    int total_items = 0, total_slots = 0;
+    int total = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      if (w == static_cast<int>(warp_id())) items += total_items, slots += total_slots;
-      total_items += sums[w][0];
-      total_slots += sums[w][1];
+      if (w == static_cast<int>(warp_id())) items += total;
+      total += sums[w];
     }
-    if (idx < at.items + total_items) {
+    if (idx < at.items + total) {
       const int first = at.items + items - own;
-      if (idx >= first && idx < first + own) {
-        const int i = idx - first;
-        shared->b = b;
-        shared->tile = i / s.chunks;
-        shared->tiles = s.tiles;
-        shared->chunk = i % s.chunks;
-        shared->chunks = s.chunks;
-        shared->slots = at.slots + slots - s.slots;
-      }
+      if (idx >= first && idx < first + own) *shared = {b, idx - first, own, 0, 1, 0};
       __syncthreads();
       *found = *shared;
       return true;
     }
-    at.items += total_items;
-    at.slots += total_slots;
+    at.items += total;
   }
   return false;
 }

@@ -141,13 +141,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Att
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dirty + L::kStages);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* spoiled = abort_flag + 1;
-  __shared__ int sums[kThreads / 32][2];
+  __shared__ int sums[kThreads / 32];
   __shared__ Found found;
 
   const int tid = threadIdx.x, lane = lane_id();
   const int warp = __shfl_sync(0xffffffffu, warp_id(), 0);  // known to be the same for the warp
   const int hk = blockIdx.x % p.kv_heads;  // heads side by side: the heaviest tiles of all of them start first
-  Search at{0, 0, 0, key_chunk(p)};
+  Search at{0, 0, key_chunk(p)};
   Found f;
   if (!find_item<kThreads / 32>(p, at, blockIdx.x / p.kv_heads, &found, sums, &f)) return;
   int qs, ql, ks, kl;

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* empty = full + L::kStages;
-  __shared__ int sums[kWarps][2];
+  __shared__ int sums[kWarps];
   __shared__ Found found;
   __shared__ long long line_sums[kWarps][3];
   __shared__ Part line_part;
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
   }
   uint32_t used = 0;    // key tiles since the kernel's start
   uint32_t issued = 0;  // ... and how many of them thread 0 has asked for
-  Search at{0, 0, 0, p.chunk};
+  Search at{0, 0, p.chunk};
   for (int item = blockIdx.x / kStepCluster;; item += gridDim.x) {
     Found f{};
     Part part{};
@@ -444,8 +444,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
 template <class T, int DP, int WIDE, int SPLIT>
 __global__ void __launch_bounds__(WIDE * SPLIT * 32) attention_join_kernel(const AttnParams p) {
   constexpr int kJoinWarps = WIDE * SPLIT;
-  __shared__ int sums[kJoinWarps];
   __shared__ Shares own;
+  __shared__ int own_before;
   __shared__ long long line_sums[kJoinWarps][3];
   __shared__ float warp_ml[kJoinWarps][2];
   __shared__ float warp_o[kJoinWarps][DP];
@@ -461,24 +461,18 @@ __global__ void __launch_bounds__(WIDE * SPLIT * 32) attention_join_kernel(const
     if (!ql) return;
     line = line_of<kJoinWarps>(p, b, line_sums);
   } else {
-    // the sequence's shares and the slots before its own: up to 32 sequences by the
+    // the sequence's shares and the slots before its own, of up to 32 sequences: by the
     // first warp, since the others have the same to find
-    if (p.batch > 32 || warp == 0) {
-      const int chunk = key_chunk(p), step = p.batch > 32 ? kJoinWarps * 32 : 32;
+    if (warp == 0) {
+      const int chunk = key_chunk(p);
       s = shares_of(p, b, chunk);
-      if (s.slots)
-        for (int j = threadIdx.x; j < b; j += step) before += shares_of(p, j, chunk).slots;
+      if (lane < b) before = shares_of(p, lane, chunk).slots;
       before = __reduce_add_sync(0xffffffffu, before);
-    }
-    if (lane == 0) {
-      sums[warp] = before;
-      if (warp == 0) own = s;
+      if (lane == 0) own = s, own_before = before;
     }
     __syncthreads();
     s = own;
-    before = 0;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) before += sums[w];
+    before = own_before;
     if (!s.slots || before + s.slots > p.max_slots) return;
   }
   constexpr int kPer = DP / 32;
@@ -496,7 +490,7 @@ __global__ void __launch_bounds__(WIDE * SPLIT * 32) attention_join_kernel(const
     float top = -INFINITY, total = 0.f, o[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int c = warp % SPLIT; c < shares; c += SPLIT) {
       const int at = WIDE == 1 ? 2 * (first + c) + (c == 0) : first + c;
       const size_t slot = (static_cast<size_t>(at) * p.kv_heads + hk) * p.tile_rows + r;

@@ -386,3 +386,11 @@ def test_scores_of_minus_infinity(q_lengths, k_lengths, kv_heads, dim, dtype, ev
     want, bound = ops.attention(q, k, v, q_lengths, k_lengths, True)
     assert want.isnan().any() or not every
     ops.check(o, want, bound)
+
+
+@pytest.mark.parametrize("batch", [31, 32, 33, 34])
+def test_more_sequences_than_lanes_in_clusters(batch):
+    """Lone tokens of few keys with one key head: eight CTAs a sequence, however many sequences find place."""
+    k_lengths = [(97 * i) % 500 for i in range(batch)]
+    check(43, [1] * batch, k_lengths, 1, 1, 128, BF16, True)
+    check(44, [0 if i % 3 == 1 else 1 for i in range(batch)], k_lengths, 4, 1, 64, F16, True)
