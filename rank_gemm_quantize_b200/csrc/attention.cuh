@@ -146,9 +146,9 @@ __device__ __forceinline__ int warp_inclusive(int v) {
 
 // The keys of a share where the host left it open (few row tiles, up to 32
 // sequences): the longest sequence's keys cut into as many shares as still run at
-// once, each of 512 keys or more. The lengths are on the device, so every CTA
-// works it out for itself, and all come to the same.
-constexpr int kAutoShares = 16;
+// once, each of 512 keys or more; a warp's lanes try 1 to 31 (a lone sequence of 64000
+// keys, one key head, 32 rows: 43 us, with 16 at most 62). The lengths are on the
+// device, so every CTA works it out for itself, and all come to the same.
 __device__ __forceinline__ int key_chunk(const AttnParams& p) {
   if (p.chunk) return p.chunk;
   const int lane = lane_id();
@@ -170,7 +170,7 @@ __device__ __forceinline__ int key_chunk(const AttnParams& p) {
     const int k = __shfl_sync(0xffffffffu, keys, b);
     ctas += __shfl_sync(0xffffffffu, tiles, b) * (k > c ? (k + c - 1) / c : 1);
   }
-  const unsigned fails = __ballot_sync(0xffffffffu, lane > 0 && (c < 512 || ctas > p.fill || lane >= kAutoShares));
+  const unsigned fails = __ballot_sync(0xffffffffu, lane > 0 && (c < 512 || ctas > p.fill || lane == 31));
   const int chunk = fails & 2u ? longest + 1 : __shfl_sync(0xffffffffu, c, __ffs(fails) - 2);
   return chunk;
 }
@@ -244,8 +244,11 @@ constexpr int kPromptKeys = 128;
 // together whatever the lengths are, and only the units at a stretch's ends are in
 // parts: the part that begins a unit goes to slot 2 cta + 1, any other to slot 2 cta.
 // (64 tokens on 200 to 16000 keys, 8 key heads: 156 us; shares of equal length dealt
-// out in turn 168. 16 on 4000 each: 50 and 57; on 1000 each 16.4 and 15.0. kEnds 2:
-// 160 us, 8: 160. kLeast 8: 20 tokens on 30 to 12000 keys, 4 key heads, 15.8 us, 5: 14.0.)
+// out in turn 168. 16 on 4000 keys each: 50 and 57. Not all calls gain: 16 on 1000 each
+// 16.8 and 15.0, 16 on 200 each 13.4 and 10.5, 6 on 30 to 12000 17.4 and 15.6; no cuts
+// where a unit has kLeast tiles or fewer on average: 16 on 200 each 12.0, but 12 on 20
+// to 700 15.3 for 12.9. kEnds 2: 160 us, 8: 160. kLeast 8: 20 tokens on 30 to 12000
+// keys, 4 key heads, 15.8 us, 5: 14.0.)
 struct Line {
   long long places;  // of all units
   long long before;  // ... before sequence b

@@ -394,3 +394,10 @@ def test_more_sequences_than_lanes_in_clusters(batch):
     k_lengths = [(97 * i) % 500 for i in range(batch)]
     check(43, [1] * batch, k_lengths, 1, 1, 128, BF16, True)
     check(44, [0 if i % 3 == 1 else 1 for i in range(batch)], k_lengths, 4, 1, 64, F16, True)
+
+
+@pytest.mark.parametrize("q_lengths,k_lengths", [([40], [8200]), ([40], [15900]), ([33, 20], [16384, 40]), ([64], [40000])])
+def test_more_shares_of_one_sequence(q_lengths, k_lengths):
+    """One key head, so that the keys of a row tile go to as many CTAs as a share of 512 keys, or a warp, allows."""
+    check(45, q_lengths, k_lengths, 1, 1, 64, BF16, True)
+    check(46, [n // 4 for n in q_lengths], k_lengths, 8, 1, 128, F16, False)
