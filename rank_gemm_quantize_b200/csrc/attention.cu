@@ -66,19 +66,21 @@ svdq_status plan(const svdq_attention_args* c, Plan* out) {
   }
   const long long rows = static_cast<long long>(c->q_rows) * (c->q_heads / c->kv_heads);
   // Eight CTAs an item where all of those run at once, up to 1024 keys each (a lone
-  // token, 4 key heads: of 777 keys 6.1 us, as shares and a join 9.0; of 8000 14.4 and
-  // 14.1; of 16000 24 and 15). Else the kernel for many queries where a sequence
+  // token, 4 key heads: of 777 keys 6.1 us, as stretches and a join 12.3; of 8000 14.6
+  // and 13.1; of 16000 24.9 and 14.6). Else the kernel for many queries where a sequence
   // has more than one tile of rows on average, since each reads the keys again (32
-  // rows, 4000 keys, 64 sequences of 8 key heads: 228 us, the kernel for few 262; 16
-  // rows 189 so; 24 rows, 4 sequences: 28 and 26).
+  // rows, 4000 keys, 64 sequences of 8 key heads: 229 us, the kernel for few 353; 24 rows
+  // of 1000 keys 86 and 110; 24 rows, 4 sequences of 4000: 28 and 24).
   p.cluster = (rows / kStepRows + c->batch) * c->kv_heads * kStepCluster <= 2 * p.sms &&
               c->k_rows <= static_cast<long long>(1024) * kStepCluster * c->batch;
   p.prompt = !p.cluster && rows > static_cast<long long>(kStepRows) * c->batch;
   const int key_tile = p.prompt ? kPromptKeys : kStepKeys, tile_rows = p.prompt ? kPromptRows : kStepRows;
   long long slots = 0;  // partial results
   if (p.prompt) {
-    // where the row tiles alone leave SMs idle, the kernel cuts the keys (key_chunk);
-    // its shares are no more than the CTAs that run at once
+    // where the row tiles alone leave SMs idle, the kernel cuts the keys (key_chunk); its
+    // shares are no more than the CTAs that run at once. One warp finds them, a lane a
+    // sequence, hence 32 (32 rows on 16000 keys, one key head: 32 sequences 75 us, 33,
+    // whose keys are not cut, 199)
     const long long tiles = rows / kPromptRows;
     p.fill = p.sms / c->kv_heads;
     p.open = c->batch <= 32 && tiles < p.fill && c->k_rows > 768;  // of fewer keys no share would have 512
