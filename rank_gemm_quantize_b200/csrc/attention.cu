@@ -37,6 +37,12 @@ svdq_status check(const svdq_attention_args* c) {
   // rows and row-head pairs are counted in int
   if (static_cast<long long>(c->q_rows) * c->q_heads > 1ll << 30 || c->k_rows > 1 << 30)
     return fail(SVDQ_ERR_UNSUPPORTED, "q_rows x q_heads or k_rows exceeds 2^30");
+  // The places of the line of work (Line) times its CTAs are counted in 64 bits. Offsets
+  // that overlap can give each sequence all rows and all keys.
+  const double rows = static_cast<double>(c->q_rows) * (c->q_heads / c->kv_heads);
+  if (rows <= static_cast<double>(kStepRows) * c->batch &&
+      c->batch * (rows / kStepRows + 1) * (c->k_rows / kStepKeys + 1. + Line::kEnds) > static_cast<double>(1ll << 52))
+    return fail(SVDQ_ERR_UNSUPPORTED, "batch x q_rows x k_rows is too large");
   const long long strides[] = {c->q_row_stride, c->q_head_stride, c->k_row_stride, c->k_head_stride, c->v_row_stride, c->v_head_stride};
   const int extent[] = {c->q_rows, c->q_heads, c->k_rows, c->kv_heads, c->k_rows, c->kv_heads};
   for (int i = 0; i < 6; ++i)  // the stride of a single row or head is not used

@@ -267,7 +267,7 @@ __device__ __forceinline__ Units units_of(const AttnParams& p, int b) {
   seq_extent(p.k_offsets, b, p.k_rows, start, kl);
   return {(ql * p.group + kStepRows - 1) / kStepRows, max(1, (kl + kStepKeys - 1) / kStepKeys)};
 }
-// Sum of values from 0 to 2^50 over the warp, in two parts of 24 and 26 bits.
+// Sum over the warp of values from 0 up, together 2^52 at most, in two parts of 24 and 28 bits.
 __device__ __forceinline__ long long warp_sum(long long v) {
   const unsigned low = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v & 0xFFFFFF));
   const unsigned high = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v >> 24));

@@ -135,3 +135,12 @@ def test_binding_refuses_unknown_names(rq):
 @pytest.mark.parametrize("kernels", [-1, 3])
 def test_selftest_refuses_unknown_kernels(rq, kernels):
     refused(rq, rq.lib().svdq_selftest_operator_wait(kernels, None), INVALID, b"kernels")
+
+
+def test_attention_refuses_work_that_passes_64_bits(rq):
+    """Overlapping offsets can give each of 65535 sequences 2^16 row tiles and 2^24 key tiles."""
+    c = attention_args(rq, batch=65535, q_rows=65535, q_heads=16, kv_heads=1, q_row_stride=1024, k_row_stride=64, v_row_stride=64,
+                       k_rows=1 << 30)
+    n = ctypes.c_size_t()
+    refused(rq, rq.lib().svdq_attention_workspace_size(ctypes.byref(c), ctypes.byref(n)), UNSUPPORTED, b"too large")
+    refused(rq, rq.lib().svdq_attention_forward(ctypes.byref(c), None), UNSUPPORTED, b"too large")
