@@ -57,7 +57,7 @@ struct Plan {
   bool cluster;  // attention_step.cu: an item's shares are a cluster
   bool open;     // attention_prompt.cu: the kernel sets `chunk`
   int fill;
-  size_t ml, total;
+  size_t ml, cuts, total;  // bytes of the partial results, of their maxima and sums too, and of all
 };
 
 // Which kernel, and the shares the keys are cut into. The lengths of the
@@ -95,14 +95,15 @@ svdq_status plan(const svdq_attention_args* c, Plan* out) {
     // two CTAs an SM, no more than there are stretches (Line) that are worth one
     const long long units = rows / kStepRows + c->batch;
     p.ctas = static_cast<int>(std::min(std::max(1ll, 2ll * p.sms / c->kv_heads), units + c->k_rows / (Line::kLeast * kStepKeys)));
-    slots = 2ll * p.ctas;
+    slots = p.ctas > 1 ? 2ll * p.ctas : 0;
   }
   p.chunk = std::max(1, (c->k_rows + key_tile - 1) / key_tile) * key_tile;
   if ((slots + rows / tile_rows + c->batch) * c->kv_heads > 0x7fffffffll) return fail(SVDQ_ERR_UNSUPPORTED, "too many sequences times heads");
   p.max_slots = static_cast<int>(slots);
   const size_t slot_rows = static_cast<size_t>(slots) * c->kv_heads * tile_rows;
   p.ml = slot_rows * (c->head_dim <= 64 ? 64 : 128) * 4;
-  p.total = p.ml + slot_rows * 8;
+  p.cuts = p.ml + slot_rows * 8;
+  p.total = p.cuts + (p.prompt || !slots ? 0 : p.ctas * sizeof(Cut));
   *out = p;
   return SVDQ_OK;
 }
@@ -168,6 +169,7 @@ svdq_status svdq_attention_forward(const svdq_attention_args* a, void* stream) {
   p.max_slots = pl.max_slots;
   p.part = static_cast<float*>(a->workspace);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + pl.ml);
+  p.cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(a->workspace) + pl.cuts);
   AttnMaps maps{};
   const int key_tile = pl.prompt ? kPromptKeys : kStepKeys;
   if (a->k_rows > 0 && (!make_kv_map(&maps.k, a, a->k, a->k_row_stride, a->k_head_stride, key_tile) ||

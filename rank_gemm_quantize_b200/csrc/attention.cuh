@@ -7,6 +7,7 @@
 
 namespace svdq {
 
+struct Cut;
 struct AttnParams {
   const void *q, *v;  // v for the values that a product with 0 would spoil; tiles come by TMA
   void* out;          // [q_rows, q_heads, dim]
@@ -22,6 +23,12 @@ struct AttnParams {
   int ctas;           // attention_step.cu: CTAs a key head
   int max_slots;      // partial results (tile_rows rows each) the workspace holds
   float *part, *part_ml;
+  Cut* cuts;   // attention_step.cu: [ctas]
+};
+// A row tile that is in parts, as the second CTA that works on it notes it for the join.
+struct Cut {
+  int unit, first, shares, b;  // row tile, the first CTA, how many CTAs (0: none is noted), sequence
+  int qs, ql, kl, none;        // the sequence's first query, its queries and keys
 };
 struct AttnMaps {
   CUtensorMap k, v;   // [k_rows][kv_heads][dim], box {64, 1, key tile}, 128-byte swizzle, zero fill
@@ -244,14 +251,14 @@ constexpr int kPromptKeys = 128;
 // together whatever the lengths are, and only the units at a stretch's ends are in
 // parts: the part that begins a unit goes to slot 2 cta + 1, any other to slot 2 cta.
 // (64 tokens on 200 to 16000 keys, 8 key heads: 156 us; shares of equal length dealt
-// out in turn 168. 16 on 4000 keys each: 50 and 57. Not all calls gain: 16 on 1000 each
-// 16.8 and 15.0, 16 on 200 each 13.4 and 10.5, 6 on 30 to 12000 17.4 and 15.6; no cuts
-// where a unit has kLeast tiles or fewer on average: 16 on 200 each 12.0, but 12 on 20
-// to 700 15.3 for 12.9. kEnds 2: 160 us, 8: 160. kLeast 8: 20 tokens on 30 to 12000
-// keys, 4 key heads, 15.8 us, 5: 14.0.)
+// out in turn 166. 16 on 4000 keys each: 50 and 58. Short sequences of one length lose by
+// it: 16 on 1000 each 16.1 and 15.1, 16 on 200 each 12.6 and 10.7; no cuts where a unit
+// has kLeast tiles or fewer on average would help those, but 12 tokens on 20 to 700 keys
+// then take 2.4 us more. kEnds 2: 20 tokens on 30 to 12000 keys, 4 key heads, 21.2 us, 4:
+// 18.2; 8: the 64 tokens 160. kLeast 8: 6 tokens, 8 key heads, 13.9 us, 5: 11.5; 3: the 20
+// tokens 18.4.)
 struct Line {
   long long places;  // of all units
-  long long before;  // ... before sequence b
   int ctas;          // that share it: one a unit and one per kLeast key tiles, as far as they go
   static constexpr int kLeast = 5, kEnds = 4;
   __device__ __forceinline__ long long begin(int cta) const { return places * cta / ctas; }
@@ -275,28 +282,26 @@ __device__ __forceinline__ long long warp_sum(long long v) {
 }
 // Called by the whole CTA; `sums` is in shared memory.
 template <int WARPS>
-__device__ __forceinline__ Line line_of(const AttnParams& p, int b, long long (*sums)[3]) {
-  long long v[3] = {0, 0, 0};  // places, those before b, units
+__device__ __forceinline__ Line line_of(const AttnParams& p, long long (*sums)[2]) {
+  long long v[2] = {0, 0};  // places, units
   const bool alone = p.batch <= 32;  // each warp for itself, no barrier
   for (int j = alone ? lane_id() : threadIdx.x; j < p.batch; j += alone ? 32 : WARPS * 32) {
     const Units u = units_of(p, j);
-    const long long places = static_cast<long long>(u.units) * (u.tiles + Line::kEnds);
-    v[0] += places;
-    if (j < b) v[1] += places;
-    v[2] += u.units;
+    v[0] += static_cast<long long>(u.units) * (u.tiles + Line::kEnds);
+    v[1] += u.units;
   }
 #pragma unroll
-  for (int i = 0; i < 3; ++i) v[i] = warp_sum(v[i]);
+  for (int i = 0; i < 2; ++i) v[i] = warp_sum(v[i]);
   if (!alone) {
     if (lane_id() == 0)
-      for (int i = 0; i < 3; ++i) sums[warp_id()][i] = v[i];
+      for (int i = 0; i < 2; ++i) sums[warp_id()][i] = v[i];
     __syncthreads();
-    v[0] = v[1] = v[2] = 0;
+    v[0] = v[1] = 0;
     for (int w = 0; w < WARPS; ++w)
-      for (int i = 0; i < 3; ++i) v[i] += sums[w][i];
+      for (int i = 0; i < 2; ++i) v[i] += sums[w][i];
     __syncthreads();
   }
-  return {v[0], v[1], static_cast<int>(min(static_cast<long long>(p.ctas), v[2] + (v[0] - v[2] * Line::kEnds) / Line::kLeast))};
+  return {v[0], static_cast<int>(min(static_cast<long long>(p.ctas), v[1] + (v[0] - v[1] * Line::kEnds) / Line::kLeast))};
 }
 struct Part {
   int b, unit;       // sequence, row tile
@@ -309,7 +314,7 @@ struct LineSearch {  // sequences before b0 hold `places` places
 // The unit that place `x` of the line belongs to, x less than the line's places. Called
 // by the whole CTA with x that never decreases; `shared` and `sums` are in shared memory.
 template <int WARPS>
-__device__ __forceinline__ Part part_at(const AttnParams& p, LineSearch& at, long long x, Part* shared, long long (*sums)[3]) {
+__device__ __forceinline__ Part part_at(const AttnParams& p, LineSearch& at, long long x, Part* shared, long long (*sums)[2]) {
   const int per = p.batch <= 32 ? 32 : WARPS * 32;
   for (;; at.b0 += per) {
     const int b = at.b0 + (per == 32 ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x));
@@ -361,7 +366,7 @@ __device__ __forceinline__ Part part_at(const AttnParams& p, LineSearch& at, lon
 cudaError_t take_status_attention_prompt(int* status, cudaStream_t st);
 cudaError_t give_up_attention_prompt(cudaStream_t st);
 cudaError_t launch_attention_prompt(const AttnParams& p, const AttnMaps& maps, bool bf16, cudaStream_t st);
-// Joins the shares of the sequences that have several (after either kernel).
+// Joins the parts of the row tiles that have several (after either kernel).
 cudaError_t launch_attention_join(const AttnParams& p, bool bf16, cudaStream_t st);
 cudaError_t take_status_attention_step(int* status, cudaStream_t st);
 cudaError_t give_up_attention_step(cudaStream_t st);

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
   uint64_t* empty = full + L::kStages;
   __shared__ int sums[kWarps];
   __shared__ Found found;
-  __shared__ long long line_sums[kWarps][3];
+  __shared__ long long line_sums[kWarps][2];
   __shared__ Part line_part;
   __shared__ int spoiled;
   __shared__ int abort_word;
@@ -114,11 +114,14 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
   __syncthreads();
   if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
+  // the thread that notes for the join what this CTA has the second part of
+  const bool notes = !CLUSTER && p.max_slots && hk == 0 && tid == kThreads - 32;
   Line line{};
   LineSearch along{0, 0};
   long long x = 0, x_end = 0;  // this CTA's stretch of the line
   if (!CLUSTER) {
-    line = line_of<kWarps>(p, 0, line_sums);
+    line = line_of<kWarps>(p, line_sums);
+    if (notes) p.cuts[blockIdx.x] = Cut{};
     if (static_cast<int>(blockIdx.x) >= line.ctas) return;
     x = line.begin(blockIdx.x), x_end = line.begin(blockIdx.x + 1);
   }
@@ -184,6 +187,12 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
       for (int i = 0; i < min(tiles, L::kStages); ++i) issue(i);
     }
     issued = used + min(tiles, L::kStages);
+    if (notes && first > 0) {
+      const long long begin = line.begin(blockIdx.x) - first;  // of the unit's key tiles
+      const int cta = line.cta_of(begin);
+      if (cta + 1 == static_cast<int>(blockIdx.x))
+        p.cuts[blockIdx.x] = {part.unit, cta, line.cta_of(begin + part.tiles - 1) - cta + 1, part.b, qs, ql, kl, 0};
+    }
 
     // the rows' queries as mma operands
     uint32_t qf[DP / 16][4];
@@ -438,113 +447,118 @@ __global__ void __launch_bounds__(kThreads, 2) attention_step_kernel(const AttnP
   }
 }
 
-// Joins the shares: a row's softmax over all of them. CTA (b, key head, z) takes
-// WIDE rows at a time, z WIDE .., (z + gridDim.z) WIDE ..; SPLIT warps divide a row's
-// shares among them.
-template <class T, int DP, int WIDE, int SPLIT>
-__global__ void __launch_bounds__(WIDE * SPLIT * 32) attention_join_kernel(const AttnParams p) {
-  constexpr int kJoinWarps = WIDE * SPLIT;
-  __shared__ Shares own;
-  __shared__ int own_before;
-  __shared__ long long line_sums[kJoinWarps][3];
-  __shared__ float warp_ml[kJoinWarps][2];
-  __shared__ float warp_o[kJoinWarps][DP];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before has ended
-  const int b = blockIdx.x, hk = blockIdx.y, warp = warp_id(), lane = lane_id();
-  int qs, ql;
-  seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
-  Shares s{0, 0, 0};
-  int before = 0;
-  Line line{};
-  const int key_tiles = units_of(p, b).tiles;
-  if (WIDE == 1) {
-    if (!ql) return;
-    line = line_of<kJoinWarps>(p, b, line_sums);
-  } else {
-    // the sequence's shares and the slots before its own, of up to 32 sequences: by the
-    // first warp, since the others have the same to find
-    if (warp == 0) {
-      const int chunk = key_chunk(p);
-      s = shares_of(p, b, chunk);
-      if (lane < b) before = shares_of(p, lane, chunk).slots;
-      before = __reduce_add_sync(0xffffffffu, before);
-      if (lane == 0) own = s, own_before = before;
-    }
-    __syncthreads();
-    s = own;
-    before = own_before;
-    if (!s.slots || before + s.slots > p.max_slots) return;
-  }
-  constexpr int kPer = DP / 32;
-  const int rows = ql * p.group;
-  for (int row0 = blockIdx.z * WIDE; row0 < rows; row0 += gridDim.z * WIDE) {
-    const int row = min(row0 + warp / SPLIT, rows - 1);
-    int first = before + row / p.tile_rows * s.chunks, shares = s.chunks;
-    const int r = row % p.tile_rows;
-    if (WIDE == 1) {
-      const long long begin = line.before + static_cast<long long>(row / p.tile_rows) * (key_tiles + Line::kEnds) + Line::kEnds;
-      first = line.cta_of(begin);
-      shares = line.cta_of(begin + key_tiles - 1) - first + 1;
-      if (shares == 1) continue;  // written already
-    }
-    float top = -INFINITY, total = 0.f, o[kPer];
+// A warp's part of a row's softmax over partial results: every STEP-th of them from
+// `from` on, the slot of each by slot_of. A lane holds DP / 32 columns.
+template <int DP>
+struct Joined {
+  static constexpr int kPer = DP / 32;
+  float top = -INFINITY, total = 0.f, o[kPer] = {};
+  __device__ __forceinline__ void add(float ml_top, float ml_total, const float (&v)[kPer], float scale_log2) {
+    const float now = fmaxf(top, ml_top), base = (now == -INFINITY ? 0.f : now) * scale_log2;
+    const float was = exp2_fast(fmaf(top, scale_log2, -base)), w = exp2_fast(fmaf(ml_top, scale_log2, -base));
+    top = now;
+    total = fmaf(total, was, ml_total * w);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+    for (int e = 0; e < kPer; ++e) o[e] = fmaf(o[e], was, v[e] * w);
+  }
+  template <int STEP, class SlotOf>
+  __device__ __forceinline__ void gather(const AttnParams& p, int from, int shares, SlotOf slot_of) {
 #pragma unroll 8
-    for (int c = warp % SPLIT; c < shares; c += SPLIT) {
-      const int at = WIDE == 1 ? 2 * (first + c) + (c == 0) : first + c;
-      const size_t slot = (static_cast<size_t>(at) * p.kv_heads + hk) * p.tile_rows + r;
+    for (int c = from; c < shares; c += STEP) {
+      const size_t slot = slot_of(c);
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot);
       float v[kPer];
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) v[e] = p.part[slot * DP + kPer * lane + e];
-      const float now = fmaxf(top, ml.x), base = (now == -INFINITY ? 0.f : now) * p.scale_log2;
-      const float was = exp2_fast(fmaf(top, p.scale_log2, -base)), w = exp2_fast(fmaf(ml.x, p.scale_log2, -base));
-      top = now;
-      total = fmaf(total, was, ml.y * w);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] = fmaf(o[e], was, v[e] * w);
+      for (int e = 0; e < kPer; ++e) v[e] = p.part[slot * DP + kPer * lane_id() + e];
+      add(ml.x, ml.y, v, p.scale_log2);
     }
-    if constexpr (SPLIT > 1) {
-      static_assert(WIDE == 1, "the first warp finishes the row");
-      if (lane == 0) {
-        warp_ml[warp][0] = top;
-        warp_ml[warp][1] = total;
-      }
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) warp_o[warp][kPer * lane + e] = o[e];
-      __syncthreads();
-      top = -INFINITY;
-#pragma unroll
-      for (int a = 0; a < SPLIT; ++a) top = fmaxf(top, warp_ml[a][0]);
-      const float base = (top == -INFINITY ? 0.f : top) * p.scale_log2;
-      total = 0.f;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-#pragma unroll
-      for (int a = 0; a < SPLIT; ++a) {
-        const float w = exp2_fast(fmaf(warp_ml[a][0], p.scale_log2, -base));
-        total = fmaf(warp_ml[a][1], w, total);
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] = fmaf(warp_o[a][kPer * lane + e], w, o[e]);
-      }
-      __syncthreads();
-      if (warp > 0) continue;
-    } else if (row0 + warp >= rows) {
-      continue;
-    }
-    const float norm = row_norm(total, [&] {
-      int start, kl;
-      seq_extent(p.k_offsets, b, p.k_rows, start, kl);
-      return last_key(p, row, ql, kl);
+  }
+  // row of a sequence of ql queries, which start at qs, and kl keys
+  template <class T>
+  __device__ __forceinline__ void store(const AttnParams& p, int qs, int ql, int kl, int hk, int row) const {
+    const float norm = row_norm(total, [&] { return last_key(p, row, ql, kl); });
+    const int c = kPer * lane_id();
+    if (c >= p.dim) return;
+    T* out = static_cast<T*>(p.out) + (static_cast<size_t>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim + c;
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(Half16<T>::pack(o[0] * norm, o[1] * norm), Half16<T>::pack(o[2] * norm, o[3] * norm));
+    else
+      *reinterpret_cast<uint32_t*>(out) = Half16<T>::pack(o[0] * norm, o[1] * norm);
+  }
+};
+
+// Joins the shares of attention_prompt.cu, of up to 32 sequences (key_chunk). CTA (b, key
+// head, z) takes four rows at a time, 4 z .., 4 (z + gridDim.z) .., a warp each.
+template <class T, int DP>
+__global__ void __launch_bounds__(128) attention_join_kernel(const AttnParams p) {
+  __shared__ Shares own;
+  __shared__ int own_before;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before has ended
+  const int b = blockIdx.x, hk = blockIdx.y, warp = warp_id(), lane = lane_id();
+  int qs, ql, ks, kl;
+  seq_extent(p.q_offsets, b, p.q_rows, qs, ql);
+  seq_extent(p.k_offsets, b, p.k_rows, ks, kl);
+  // the sequence's shares and the slots before its own: by the first warp, since the
+  // others have the same to find
+  if (warp == 0) {
+    const int chunk = key_chunk(p);
+    const Shares s = shares_of(p, b, chunk);
+    const int before = __reduce_add_sync(0xffffffffu, lane < b ? shares_of(p, lane, chunk).slots : 0);
+    if (lane == 0) own = s, own_before = before;
+  }
+  __syncthreads();
+  const Shares s = own;
+  if (!s.slots || own_before + s.slots > p.max_slots) return;
+  for (int row = 4 * blockIdx.z + warp; row < ql * p.group; row += 4 * gridDim.z) {
+    const int first = own_before + row / p.tile_rows * s.chunks;
+    Joined<DP> joined;
+    joined.template gather<1>(p, 0, s.chunks, [&](int c) {
+      return (static_cast<size_t>(first + c) * p.kv_heads + hk) * p.tile_rows + row % p.tile_rows;
     });
-    if (kPer * lane < p.dim) {
-      T* out = static_cast<T*>(p.out) + (static_cast<size_t>(qs + row / p.group) * p.q_heads + hk * p.group + row % p.group) * p.dim + kPer * lane;
-      if constexpr (kPer == 4)
-        *reinterpret_cast<uint2*>(out) = make_uint2(Half16<T>::pack(o[0] * norm, o[1] * norm), Half16<T>::pack(o[2] * norm, o[3] * norm));
-      else
-        *reinterpret_cast<uint32_t*>(out) = Half16<T>::pack(o[0] * norm, o[1] * norm);
+    joined.template store<T>(p, qs, ql, kl, hk, row);
+  }
+}
+
+// Joins the parts of attention_step_kernel's units: CTA (x, key head, z) those that CTA
+// x + 1 there has noted, ROWS rows at a time, ROWS z .., ROWS (z + gridDim.z) .., each by
+// 16 / ROWS warps. (A CTA for each sequence and row, which all look for their unit: 4000
+// tokens on 200 keys, 8 key heads, 1790 us for 820; one CTA a beginning of a stretch
+// that looks for the unit there: 16 tokens 14.7 us.)
+constexpr int kJoinWarps = 16;
+template <class T, int DP, int ROWS>
+__global__ void __launch_bounds__(kJoinWarps * 32) attention_line_join_kernel(const AttnParams p) {
+  constexpr int kSplit = kJoinWarps / ROWS;
+  __shared__ float2 warp_ml[kJoinWarps];
+  __shared__ float warp_o[kJoinWarps][DP];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before has ended
+  const int hk = blockIdx.y, warp = warp_id(), lane = lane_id();
+  const Cut cut = p.cuts[blockIdx.x + 1];
+  if (!cut.shares) return;
+  const int row0 = cut.unit * kStepRows, rows = min(kStepRows, cut.ql * p.group - row0);
+  constexpr int kPer = Joined<DP>::kPer;
+  for (int r0 = ROWS * blockIdx.z; r0 < rows; r0 += ROWS * gridDim.z) {
+    const int r = r0 + warp / kSplit;
+    Joined<DP> joined;
+    if (r < rows)
+      joined.template gather<kSplit>(p, warp % kSplit, cut.shares, [&](int c) {
+        return (static_cast<size_t>(2 * (cut.first + c) + (c == 0)) * p.kv_heads + hk) * kStepRows + r;
+      });
+    if (lane == 0) warp_ml[warp] = make_float2(joined.top, joined.total);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) warp_o[warp][kPer * lane + e] = joined.o[e];
+    __syncthreads();
+    if (warp % kSplit == 0 && r < rows) {
+#pragma unroll
+      for (int a = 1; a < kSplit; ++a) {
+        const float2 ml = warp_ml[warp + a];
+        float v[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) v[e] = warp_o[warp + a][kPer * lane + e];
+        joined.add(ml.x, ml.y, v, p.scale_log2);
+      }
+      joined.template store<T>(p, cut.qs, cut.ql, cut.kl, hk, row0 + r);
     }
+    __syncthreads();
   }
 }
 
@@ -577,26 +591,29 @@ cudaError_t start(const AttnParams& p, const AttnMaps& maps, cudaStream_t st) {
 
 template <class T, int DP>
 cudaError_t join(const AttnParams& p, cudaStream_t st) {
-  // Tiles of many rows have few shares (key_chunk): a warp a row. Of few rows, each has
-  // up to hundreds: four warps a row, or 16 (one token, 250 shares: 18 us for the
-  // call, 39 with four warps).
   const long long rows = (static_cast<long long>(p.q_rows) * p.group + p.batch - 1) / p.batch;
-  const bool wide = p.tile_rows > kStepRows, many = !wide && p.ctas > 16 * p.batch;
-  const int z = static_cast<int>(std::min<long long>(wide ? (rows + 3) / 4 : rows, 4096));
-  // the launch is prepared while the shares are computed, and waits for them at its
+  const bool prompt = p.tile_rows > kStepRows;
+  // Few sequences have many parts a row: 16 warps a row (one token on 64000 keys, one key
+  // head: 15.8 us, with four warps 25.4); else four rows a CTA (16 tokens on 1000 keys, 8
+  // key heads: 16.2 us, with 16 warps a row 18.7).
+  const bool many = !prompt && p.ctas > 16 * p.batch;
+  // the launch is prepared while the parts are computed, and waits for them at its
   // start (a call takes 0.1 us less than with an ordinary launch)
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.batch, p.kv_heads, z);
-  cfg.blockDim = dim3(many ? 512 : 128);
+  if (prompt)
+    cfg.gridDim = dim3(p.batch, p.kv_heads, static_cast<unsigned>(std::min<long long>((rows + 3) / 4, 4096)));
+  else
+    cfg.gridDim = dim3(p.ctas - 1, p.kv_heads, static_cast<unsigned>(std::min<long long>(many ? rows : (rows + 3) / 4, kStepRows)));
+  cfg.blockDim = dim3(prompt ? 128 : kJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return wide   ? cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP, 4, 1>, p)
-         : many ? cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP, 1, 16>, p)
-                : cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP, 1, 4>, p);
+  return prompt ? cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP>, p)
+         : many ? cudaLaunchKernelEx(&cfg, attention_line_join_kernel<T, DP, 1>, p)
+                : cudaLaunchKernelEx(&cfg, attention_line_join_kernel<T, DP, 4>, p);
 }
 
 }  // namespace

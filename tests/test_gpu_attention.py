@@ -401,3 +401,16 @@ def test_more_shares_of_one_sequence(q_lengths, k_lengths):
     """One key head, so that the keys of a row tile go to as many CTAs as a share of 512 keys, or a warp, allows."""
     check(45, q_lengths, k_lengths, 1, 1, 64, BF16, True)
     check(46, [n // 4 for n in q_lengths], k_lengths, 8, 1, 128, F16, False)
+
+
+@pytest.mark.parametrize("kv_heads,group", [(1, 1), (2, 3), (8, 4), (20, 1)])
+@pytest.mark.parametrize("batch", [5, 40, 300])
+def test_units_in_parts(batch, kv_heads, group):
+    """Ragged tokens and pieces of few rows, some without queries or keys: stretches begin anywhere in their keys."""
+    g = torch.Generator().manual_seed(batch + kv_heads)
+    k_lengths = torch.randint(0, 20000 // batch, (batch,), generator=g).tolist()
+    k_lengths[batch // 2], k_lengths[-1] = 4000, 0
+    q_lengths = torch.randint(0, 3, (batch,), generator=g).tolist()
+    q_lengths[batch // 2] = 1 + 20 // group
+    for dim, dtype, causal in ((64, F16, True), (128, BF16, False)):
+        check(47, q_lengths, k_lengths, kv_heads * group, kv_heads, dim, dtype, causal)
