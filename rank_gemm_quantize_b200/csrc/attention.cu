@@ -71,14 +71,14 @@ svdq_status plan(const svdq_attention_args* c, Plan* out) {
     return fail(SVDQ_ERR_CUDA, "no usable current device");
   }
   const long long rows = static_cast<long long>(c->q_rows) * (c->q_heads / c->kv_heads);
-  // Eight CTAs an item where all of those run at once, up to 1024 keys each (a lone
-  // token, 4 key heads: of 777 keys 6.1 us, as stretches and a join 12.3; of 8000 14.6
-  // and 13.1; of 16000 24.9 and 14.6). Else the kernel for many queries where a sequence
+  // Eight CTAs an item where all of those run at once, up to 768 keys each (a lone
+  // token, 4 key heads: of 777 keys 6.1 us, as stretches and a join 11.4; of 5000 11.2
+  // and 12.4; of 7000 13.5 and 12.1). Else the kernel for many queries where a sequence
   // has more than one tile of rows on average, since each reads the keys again (32
-  // rows, 4000 keys, 64 sequences of 8 key heads: 229 us, the kernel for few 353; 24 rows
-  // of 1000 keys 86 and 110; 24 rows, 4 sequences of 4000: 28 and 24).
+  // rows, 4000 keys, 64 sequences of 8 key heads: 229 us, the kernel for few 334; 24 rows
+  // of 1000 keys 84 and 96; 24 rows, 4 sequences of 4000: 28 and 24).
   p.cluster = (rows / kStepRows + c->batch) * c->kv_heads * kStepCluster <= 2 * p.sms &&
-              c->k_rows <= static_cast<long long>(1024) * kStepCluster * c->batch;
+              c->k_rows <= static_cast<long long>(768) * kStepCluster * c->batch;
   p.prompt = !p.cluster && rows > static_cast<long long>(kStepRows) * c->batch;
   const int key_tile = p.prompt ? kPromptKeys : kStepKeys, tile_rows = p.prompt ? kPromptRows : kStepRows;
   long long slots = 0;  // partial results

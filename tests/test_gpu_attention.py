@@ -414,3 +414,10 @@ def test_units_in_parts(batch, kv_heads, group):
     q_lengths[batch // 2] = 1 + 20 // group
     for dim, dtype, causal in ((64, F16, True), (128, BF16, False)):
         check(47, q_lengths, k_lengths, kv_heads * group, kv_heads, dim, dtype, causal)
+
+
+@pytest.mark.parametrize("keys", [6143, 6144, 6145, 8300])
+def test_lone_tokens_on_both_sides_of_the_clusters(keys):
+    """A cluster takes a lone sequence up to eight times 768 keys, stretches and a join longer ones."""
+    check(48, [1], [keys], 8, 2, 128, BF16, True)
+    check(49, [2, 1], [keys, keys], 4, 4, 64, F16, True)
