@@ -353,7 +353,8 @@ typedef enum {
  * see never reach its result, whatever they hold (infinities and NaN
  * included). Query head h reads key head h / (q_heads / kv_heads).
  * Scores, softmax statistics and sums are float; the probabilities are rounded
- * to `dtype` for the product with V. */
+ * to `dtype` for the product with V (in SVDQ_F16, those under 2^-25 of the
+ * largest so far become 0). */
 typedef struct {
   int dtype;               /* SVDQ_BF16 or SVDQ_F16: q, k, v and out */
   int batch;               /* sequences, >= 1 */

@@ -17,13 +17,19 @@
 // 2048 cycles per 128 keys, a chain 3300 (the softmax 2100 of them, whether the
 // other tile's runs beside it or not). The exponential unit alone would need 1024
 // cycles a tile, so two of eight pairs of exponentials are computed with
-// multiply-adds (exp2_pair). 4608 x 4608 keys, 24 heads of 128: 230 us, 1136
-// TFLOP/s, 70% of a library product's rate; 8192 x 8192, 16 heads of 64: 406 us,
-// 677 TFLOP/s, where the exponentials alone take 240 us. What was slower there:
+// multiply-adds (exp2_pair). 4608 x 4608 keys, 24 heads of 128: 221 to 236 us for a few
+// calls (1105 to 1180 TFLOP/s), 259 us and 1007 TFLOP/s in a long run under the power
+// cap, 73% of a library product's rate there; 8192 x 8192, 16 heads of 64: 402 to 436 us,
+// where the exponentials alone take 240 us. Each step loads five spilled values again
+// (by the counters; they are stored outside the loop). What was slower than 230 us:
 // steps of 64 keys with two S a tile (302 us: an MMA of 64 columns takes as long as
 // one of 128), two threads a row (260), P handed over in parts of 32 and 96 keys
 // (232) or 96 and 32 (238), the second half of S loaded under the first's maximum
 // (247), and for heads of 64 P in columns of its own with S issued ahead (463 for 406).
+//
+// P is rounded to the operands' 16 bits: the tensor core multiplies V, which has 16,
+// by nothing wider. That adds up to half a step of the type to a value's error; in fp16
+// a probability under 2^-25 of the one at m becomes 0. The row's sum takes P unrounded.
 //
 // O is not rescaled whenever m grows, only when it grew by more than 2^8 since
 // the last time: P may then be up to 2^8 instead of 1, which costs no digits

@@ -10,7 +10,9 @@
 // takes 16 of them: scores by mma.m16n8k16, softmax statistics and the product
 // with V in registers, with no exchange between warps until the part's end. The
 // parts' results (unnormalised float sums, maximum, sum) go to the workspace, or
-// straight to the output where a row tile is one part. A call of so few and
+// straight to the output where a row tile is one part. The probabilities are rounded
+// to 16 bits for the product with V, which takes nothing wider; the sums take them
+// unrounded, and in fp16 one under 2^-25 of the warp's largest becomes 0. A call of so few and
 // short sequences that eight CTAs an item are all there is to gain takes one
 // launch: the eight are a cluster, cut the keys evenly and join their results
 // through distributed shared memory.
